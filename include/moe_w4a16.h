@@ -380,6 +380,130 @@ moe_status moe_w4a16_shared_expert(const uint16_t *d_x, int32_t T, int32_t H, in
                                    void *d_ws, size_t ws_bytes, hipStream_t stream);
 
 /*
+ * The layer's products on unquantized (bf16) expert weights, for what comes
+ * before packing: calibration of the input scales, comparison with the packed
+ * layer, fine-tuning.  Rows are sorted by expert as moe_route_topk leaves
+ * them: expert e holds rows d_offsets[e] .. d_offsets[e+1] - 1 of M, any
+ * number of them, none too.  All products accumulate in fp32 and round once.
+ *   d_offsets       int32 [E+1], ascending.  Rows in front of d_offsets[0] and
+ *                   from d_offsets[E] on (padding) are neither read nor
+ *                   written; values outside [0, M] count as 0 or M.
+ *   d_sorted_slots  int32 [M] or NULL.  Given: row p reads x's row
+ *                   d_sorted_slots[p] / k (x is [X][K] in token order; a slot
+ *                   outside [0, X * k) reads as zeros).  NULL: row p reads x's
+ *                   row p, X == M, k is ignored.
+ *   weights         bf16 [E][N][K]
+ *
+ * moe_grouped_linear        y [M][N]:  y = x . W^T
+ * moe_grouped_swiglu        h [M][N]:  h = silu(a) * b, a = x . gate^T,
+ *                           b = x . up^T; d_a and d_b (bf16 [M][N], or both
+ *                           NULL) keep a and b for the backward pass; h is
+ *                           taken from a and b before they are rounded
+ * moe_grouped_linear_dgrad  dx [M][K]: dx = dy . W (+ dy2 . W2 with d_dy2 and
+ *                           d_w2 given: the gate and up projections' sum)
+ * moe_grouped_swiglu_dgrad  da, db [M][K]: dh = dy . W (W the down projection
+ *                           [E][N][K]), da = dh * b * silu'(a), db = dh *
+ *                           silu(a), with a and b as moe_grouped_swiglu
+ *                           keeps them ([M][K])
+ * moe_grouped_linear_wgrad  dW fp32 [E][N][K]: dW[e] = sum of dy[p]^T x[src(p)]
+ *                           over e's rows; 0 for an expert without rows;
+ *                           accumulate == 1 adds to what d_dw holds.  d_ws of
+ *                           moe_grouped_linear_wgrad_workspace_size bytes (no
+ *                           initialisation; NULL where that is 0).
+ * The gradient of x itself (where rows were gathered) is moe_combine of dx's
+ * rows without weights.
+ *
+ * N and K multiples of 8 and at most 2^20; E <= 1024; X * K * 2 < 2^32 - 256
+ * where rows are gathered (MOE_ERR_SHAPE).  Outputs overlap neither inputs nor
+ * each other (MOE_ERR_INVALID_ARG).  M == 0 is a no-op (moe_grouped_linear_wgrad
+ * still writes dW).  Deterministic; nothing is allocated; graph-capturable.
+ * There is no upper limit on d_offsets[E] - d_offsets[0] but M, and the host
+ * never reads the offsets.
+ */
+moe_status moe_grouped_linear(const uint16_t *d_x, int32_t X, int32_t K, const uint16_t *d_w, int32_t E, int32_t N,
+                              const int32_t *d_offsets, const int32_t *d_sorted_slots, int32_t k, int32_t M,
+                              uint16_t *d_y, hipStream_t stream);
+moe_status moe_grouped_swiglu(const uint16_t *d_x, int32_t X, int32_t K, const uint16_t *d_gate,
+                              const uint16_t *d_up, int32_t E, int32_t N, const int32_t *d_offsets,
+                              const int32_t *d_sorted_slots, int32_t k, int32_t M, uint16_t *d_h, uint16_t *d_a,
+                              uint16_t *d_b, hipStream_t stream);
+moe_status moe_grouped_linear_dgrad(const uint16_t *d_dy, const uint16_t *d_w, const uint16_t *d_dy2,
+                                    const uint16_t *d_w2, int32_t M, int32_t N, int32_t E, int32_t K,
+                                    const int32_t *d_offsets, uint16_t *d_dx, hipStream_t stream);
+moe_status moe_grouped_swiglu_dgrad(const uint16_t *d_dy, const uint16_t *d_w, int32_t M, int32_t N, int32_t E,
+                                    int32_t K, const int32_t *d_offsets, const uint16_t *d_a, const uint16_t *d_b,
+                                    uint16_t *d_da, uint16_t *d_db, hipStream_t stream);
+size_t moe_grouped_linear_wgrad_workspace_size(int32_t M, int32_t N, int32_t K, int32_t E);
+moe_status moe_grouped_linear_wgrad(const uint16_t *d_dy, int32_t M, int32_t N, const uint16_t *d_x, int32_t X,
+                                    int32_t K, int32_t E, const int32_t *d_offsets, const int32_t *d_sorted_slots,
+                                    int32_t k, int32_t accumulate, float *d_dw, void *d_ws, size_t ws_bytes,
+                                    hipStream_t stream);
+
+/*
+ * One 4-bit integer weight stack: E experts of an [N, K] projection.
+ *   codes  [E][N][K/2]      byte i of a row = code(2i) | code(2i+1) << 4, 0..15
+ *   scales [E][N][K/group]  bf16 bit patterns
+ *   zeros  [E][N][K/group]  u8 zero points 0..15, or NULL (8 everywhere)
+ * Weight value: (code - zero) * scale.  group 32, 64 or 128; K % 128 == 0.
+ */
+typedef struct {
+    int32_t E, N, K, group;
+    uint8_t *codes;
+    uint16_t *scales;
+    uint8_t *zeros;
+} moe_int4_tensor;
+
+/*
+ * Quantize fp32 master weights to that layout (load time).  Per group, in
+ * fp32 with correctly rounded operations:
+ *   with zeros:  lo = min(0, min W), hi = max(0, max W), s = bf16((hi - lo) / 15),
+ *                z = clamp(rint(-lo / s), 0, 15)
+ *   without:     s = bf16(max|W| / 7), z = 8
+ *   s == 0 becomes 1;  code = clamp(rint(W / s) + z, 0, 15)
+ * (rint: ties to even.)  moe_int4_dequantize is the test hook: fp32 [E][N][K].
+ */
+moe_status moe_int4_quantize_pack(const float *d_w, const moe_int4_tensor *out, hipStream_t stream);
+moe_status moe_int4_dequantize(const moe_int4_tensor *t, float *d_w_out, hipStream_t stream);
+
+/*
+ * Product of bf16 rows with 4-bit integer weights, beside moe_w4a16_linear's
+ * NVFP4: out[p] = bf16(sum_g scale_g sum_{k in g} (code - zero) x), the inner
+ * products exact and accumulated in fp32, no weight rounded.
+ *   d_offsets NULL: a dense projection of x [X][K], E == 1, X == M, no sorted
+ *   slots; given: rows by expert, with d_sorted_slots as in moe_grouped_linear.
+ *   d_out bf16 [M][N].  Any N; M == 0 is a no-op.  Weights are streamed once
+ *   per block of rows: the form for decode.  Deterministic; graph-capturable.
+ */
+moe_status moe_int4_linear(const uint16_t *d_x, int32_t X, const moe_int4_tensor *w, const int32_t *d_offsets,
+                           const int32_t *d_sorted_slots, int32_t k, int32_t M, uint16_t *d_out,
+                           hipStream_t stream);
+
+/*
+ * The routing-weighted combine that ends the layer, on its own, and its
+ * gradients:
+ *   moe_combine           out[t] = sum_j w[t][j] * y[slot_pos[t*k+j]]
+ *   moe_combine_backward  dy[slot_pos[t*k+j]] = w[t][j] * dout[t]
+ *                         dw[t][j] = <dout[t], y[slot_pos[t*k+j]]>  (fp32)
+ *                         dlogits[t][e] = w_j (dw_j - sum_i w_i dw_i) for e =
+ *                         ids[t][j], else 0 (fp32 [T][E]): the gradient of the
+ *                         router logits behind moe_route_topk's softmax over
+ *                         the k selected
+ *   d_y [M][H] bf16 rows by expert, d_slot_pos int32 [T*k] as moe_route_topk
+ *   leaves it; a position outside [0, M) is a dropped slot: it adds nothing,
+ *   its dw is 0.  Positions inside are distinct.  Rows of dy that no slot
+ *   names are not written.
+ *   d_w fp32 [T][k], or NULL: all 1.  d_dw and d_dlogits may be NULL (y is
+ *   then not read); d_dlogits needs d_w and d_topk_ids (int32 [T][k]).
+ *   H % 8 == 0, k <= 32, T <= 2^23.  T == 0 is a no-op.  Sums in fp32 in slot
+ *   order; deterministic; graph-capturable.
+ */
+moe_status moe_combine(const uint16_t *d_y, int32_t M, int32_t H, const int32_t *d_slot_pos, const float *d_w,
+                       int32_t T, int32_t k, uint16_t *d_out, hipStream_t stream);
+moe_status moe_combine_backward(const uint16_t *d_dout, int32_t T, int32_t H, const uint16_t *d_y, int32_t M,
+                                const int32_t *d_slot_pos, const float *d_w, const int32_t *d_topk_ids, int32_t k,
+                                int32_t E, uint16_t *d_dy, float *d_dw, float *d_dlogits, hipStream_t stream);
+
+/*
  * Benchmarking and test hook: which grouped-GEMM kernels run the shapes the
  * decode kernels do not take.  0: operands staged through registers, one
  * K stage in flight, for both products; 1: operands streamed to LDS by DMA

@@ -7,9 +7,11 @@ There is no CPU fallback: if the library is missing, loading raises.
 """
 
 import ctypes
+import functools
 import os
 import re
 from dataclasses import dataclass
+from typing import Optional
 
 import torch
 
@@ -35,11 +37,17 @@ class NVFP4TensorC(ctypes.Structure):
                 ("global_scale", ctypes.c_void_p)]
 
 
+class Int4TensorC(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p)]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _S = ctypes.c_size_t
 _TP = ctypes.POINTER(NVFP4TensorC)
+_IP = ctypes.POINTER(Int4TensorC)
 
 _SIGS = {
     "moe_status_string": (ctypes.c_char_p, [_I]),
@@ -70,6 +78,17 @@ _SIGS = {
                                              _P]),
     "moe_router_route_workspace_size": (_S, [_I, _I, _I]),
     "moe_router_route_topk": (_I, [_P, _I, _I, _P, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P]),
+    "moe_grouped_linear": (_I, [_P, _I, _I, _P, _I, _I, _P, _P, _I, _I, _P, _P]),
+    "moe_grouped_swiglu": (_I, [_P, _I, _I, _P, _P, _I, _I, _P, _P, _I, _I, _P, _P, _P, _P]),
+    "moe_grouped_linear_dgrad": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P]),
+    "moe_grouped_swiglu_dgrad": (_I, [_P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "moe_grouped_linear_wgrad_workspace_size": (_S, [_I, _I, _I, _I]),
+    "moe_grouped_linear_wgrad": (_I, [_P, _I, _I, _P, _I, _I, _I, _P, _P, _I, _I, _P, _P, _S, _P]),
+    "moe_int4_quantize_pack": (_I, [_P, _IP, _P]),
+    "moe_int4_dequantize": (_I, [_IP, _P, _P]),
+    "moe_int4_linear": (_I, [_P, _I, _IP, _P, _P, _I, _I, _P, _P]),
+    "moe_combine": (_I, [_P, _I, _I, _P, _P, _I, _I, _P, _P]),
+    "moe_combine_backward": (_I, [_P, _I, _I, _P, _I, _P, _P, _P, _I, _I, _P, _P, _P, _P]),
     "moe_profile_begin": (_I, [_I]),
     "moe_profile_end": (_I, [_P, _P, _P, _I]),
 }
@@ -515,3 +534,293 @@ def moe_router_route_topk(x_bits, wr_bits, k, logits=None, routing=None, ws=None
                                        _ptr(routing.sorted_slots), _ptr(routing.slot_pos), _ptr(ws), ws.numel(),
                                        _stream(stream)), "moe_router_route_topk")
     return logits, routing
+
+
+# ---------------------------------------------------------------- unquantized and 4-bit integer experts
+def _entry(fn):
+    """Runs an entry point on the device of its first tensor and on `stream`
+    (default: that device's current stream): outputs and workspaces that the
+    call allocates belong to the stream that the kernels run on."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        if not isinstance(first, torch.Tensor) and not isinstance(first, Int4Tensor):
+            raise ValueError(f"{fn.__name__}: expected a torch.Tensor, got {type(first).__name__}")
+        dev = first.device
+        if dev.type != "cuda":
+            raise ValueError(f"{fn.__name__}: expected a device (cuda) tensor, got {dev}")
+        if stream is None:
+            if dev.index == torch.cuda.current_device():
+                return fn(first, *args, **kw)
+            with torch.cuda.device(dev):
+                return fn(first, *args, **kw)
+        if stream.device != dev:
+            raise ValueError(f"stream: on {stream.device}, the tensors are on {dev}")
+        with torch.cuda.stream(stream):
+            return fn(first, *args, **kw)
+    return call
+
+
+def _same(t, name, like, dtype, shape):
+    """A contiguous tensor on `like`'s device, of that dtype (or one of them)
+    and shape; its address."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.device != like.device:
+        raise ValueError(f"{name}: on {t.device}, expected {like.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _dims(t, name, n):
+    if not isinstance(t, torch.Tensor) or t.dim() != n:
+        raise ValueError(f"{name}: expected a {n}-dimensional torch.Tensor")
+    return t.shape
+
+
+def _new(out, name, like, dtype, shape):
+    """`out` checked, or a new tensor."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _same(out, name, like, _BITS16 if dtype in _BITS16 else dtype, shape)
+    return out
+
+
+def _here():
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _rows(x, sorted_slots):
+    """(rows of the result, address of the sorted slots or None)."""
+    if sorted_slots is None:
+        return x.shape[0], None
+    M, = _dims(sorted_slots, "sorted_slots", 1)
+    return M, _same(sorted_slots, "sorted_slots", x, torch.int32, (M,))
+
+
+@_entry
+def moe_grouped_linear(x, w, offsets, sorted_slots=None, k=1, out=None):
+    """y = x . W^T by expert: x bf16 [X, K] (values or bits), w [E, N, K],
+    offsets int32 [E + 1]; with sorted_slots (int32 [M]) row p of the result
+    reads x's row sorted_slots[p] // k.  Returns [M, N] in x's dtype."""
+    (X, K), (E, N, _) = _dims(x, "x", 2), _dims(w, "w", 3)
+    px, pw = _same(x, "x", x, _BITS16, (X, K)), _same(w, "w", x, _BITS16, (E, N, K))
+    po = _same(offsets, "offsets", x, torch.int32, (E + 1,))
+    M, ps = _rows(x, sorted_slots)
+    out = _new(out, "out", x, x.dtype, (M, N))
+    _check(lib().moe_grouped_linear(px, X, K, pw, E, N, po, ps, k, M, out.data_ptr(), _here()), "moe_grouped_linear")
+    return out
+
+
+@_entry
+def moe_grouped_swiglu(x, gate, up, offsets, sorted_slots=None, k=1, h=None, a=None, b=None, save=False):
+    """h = silu(x . gate^T) * (x . up^T) by expert, rows as in
+    moe_grouped_linear.  Returns h, or (h, a, b) with save (or with a and b
+    given): the two products, for moe_grouped_swiglu_dgrad."""
+    (X, K), (E, N, _) = _dims(x, "x", 2), _dims(gate, "gate", 3)
+    px = _same(x, "x", x, _BITS16, (X, K))
+    pg, pu = _same(gate, "gate", x, _BITS16, (E, N, K)), _same(up, "up", x, _BITS16, (E, N, K))
+    po = _same(offsets, "offsets", x, torch.int32, (E + 1,))
+    M, ps = _rows(x, sorted_slots)
+    save = save or a is not None or b is not None
+    h = _new(h, "h", x, x.dtype, (M, N))
+    if save:
+        a, b = _new(a, "a", x, x.dtype, (M, N)), _new(b, "b", x, x.dtype, (M, N))
+    _check(lib().moe_grouped_swiglu(px, X, K, pg, pu, E, N, po, ps, k, M, h.data_ptr(), a.data_ptr() if save else None,
+                                    b.data_ptr() if save else None, _here()), "moe_grouped_swiglu")
+    return (h, a, b) if save else h
+
+
+@_entry
+def moe_grouped_linear_dgrad(dy, w, offsets, dy2=None, w2=None, out=None):
+    """dx = dy . W (+ dy2 . W2) by expert: dy [M, N], w [E, N, K] -> [M, K]
+    in dy's dtype."""
+    (M, N), (E, _, K) = _dims(dy, "dy", 2), _dims(w, "w", 3)
+    pd, pw = _same(dy, "dy", dy, _BITS16, (M, N)), _same(w, "w", dy, _BITS16, (E, N, K))
+    po = _same(offsets, "offsets", dy, torch.int32, (E + 1,))
+    if (dy2 is None) != (w2 is None):
+        raise ValueError("dy2 and w2 go together")
+    pd2 = pw2 = None
+    if dy2 is not None:
+        pd2, pw2 = _same(dy2, "dy2", dy, _BITS16, (M, N)), _same(w2, "w2", dy, _BITS16, (E, N, K))
+    out = _new(out, "out", dy, dy.dtype, (M, K))
+    _check(lib().moe_grouped_linear_dgrad(pd, pw, pd2, pw2, M, N, E, K, po, out.data_ptr(), _here()),
+           "moe_grouped_linear_dgrad")
+    return out
+
+
+@_entry
+def moe_grouped_swiglu_dgrad(dy, w, a, b, offsets, da=None, db=None):
+    """(da, db): the gradient through the down projection w [E, N, K] and
+    SwiGLU, with a and b [M, K] as moe_grouped_swiglu saved them."""
+    (M, N), (E, _, K) = _dims(dy, "dy", 2), _dims(w, "w", 3)
+    pd, pw = _same(dy, "dy", dy, _BITS16, (M, N)), _same(w, "w", dy, _BITS16, (E, N, K))
+    pa, pb = _same(a, "a", dy, _BITS16, (M, K)), _same(b, "b", dy, _BITS16, (M, K))
+    po = _same(offsets, "offsets", dy, torch.int32, (E + 1,))
+    da, db = _new(da, "da", dy, dy.dtype, (M, K)), _new(db, "db", dy, dy.dtype, (M, K))
+    _check(lib().moe_grouped_swiglu_dgrad(pd, pw, M, N, E, K, po, pa, pb, da.data_ptr(), db.data_ptr(), _here()),
+           "moe_grouped_swiglu_dgrad")
+    return da, db
+
+
+@_entry
+def moe_grouped_linear_wgrad(dy, x, offsets, sorted_slots=None, k=1, out=None, accumulate=False, ws=None):
+    """dW[e] = sum over e's rows of dy[p]^T x[p] (x's row sorted_slots[p] // k
+    if given): dy [M, N], x [X, K] -> fp32 [E, N, K].  accumulate adds to
+    `out`, which must be given.  ws: a workspace of
+    moe_grouped_linear_wgrad_workspace_size bytes (allocated if None)."""
+    (M, N), (X, K), E = _dims(dy, "dy", 2), _dims(x, "x", 2), _dims(offsets, "offsets", 1)[0] - 1
+    pd, px = _same(dy, "dy", dy, _BITS16, (M, N)), _same(x, "x", dy, _BITS16, (X, K))
+    po = _same(offsets, "offsets", dy, torch.int32, (E + 1,))
+    rows, ps = _rows(x, sorted_slots)
+    if rows != M:
+        raise ValueError(f"dy has {M} rows, {'x' if sorted_slots is None else 'sorted_slots'} {rows}")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    out = _new(out, "out", dy, torch.float32, (E, N, K))
+    L = lib()
+    need = L.moe_grouped_linear_wgrad_workspace_size(M, N, K, E)
+    if ws is None and need:
+        ws = torch.empty((need,), dtype=torch.uint8, device=dy.device)
+    if ws is not None:
+        _dev_tensor(ws, "ws", min_bytes=need)
+        _same(ws, "ws", dy, ws.dtype, ws.shape)
+    _check(L.moe_grouped_linear_wgrad(pd, M, N, px, X, K, E, po, ps, k, int(bool(accumulate)), out.data_ptr(),
+                                      None if ws is None else ws.data_ptr(),
+                                      0 if ws is None else ws.numel() * ws.element_size(), _here()),
+           "moe_grouped_linear_wgrad")
+    return out
+
+
+def moe_grouped_linear_wgrad_workspace_size(M, N, K, E):
+    return int(lib().moe_grouped_linear_wgrad_workspace_size(M, N, K, E))
+
+
+@dataclass
+class Int4Tensor:
+    """E experts of an [N, K] 4-bit integer projection (device)."""
+    codes: torch.Tensor                     # uint8 [E, N, K/2]
+    scales: torch.Tensor                    # bf16 (values or bits) [E, N, K/group]
+    zeros: Optional[torch.Tensor] = None    # uint8 [E, N, K/group], None: 8 everywhere
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    @property
+    def shape(self):
+        E, N, half = self.codes.shape
+        return E, N, half * 2
+
+    @property
+    def group(self):
+        return self.shape[2] // max(self.scales.shape[-1], 1)
+
+    def cstruct(self, like=None):
+        like = self.codes if like is None else like
+        _dims(self.codes, "codes", 3)
+        _dims(self.scales, "scales", 3)
+        E, N, K = self.shape
+        groups = self.scales.shape[-1]
+        if groups < 1 or K % groups:
+            raise ValueError(f"scales: {groups} groups for {K} columns")
+        pc = _same(self.codes, "codes", like, torch.uint8, (E, N, K // 2))
+        ps = _same(self.scales, "scales", like, _BITS16, (E, N, groups))
+        pz = None if self.zeros is None else _same(self.zeros, "zeros", like, torch.uint8, (E, N, groups))
+        return Int4TensorC(E, N, K, K // groups, pc, ps, pz)
+
+    @staticmethod
+    def empty(E, N, K, group=128, zeros=True, device="cuda"):
+        def u8(*s):
+            return torch.empty(s, dtype=torch.uint8, device=device)
+        return Int4Tensor(u8(E, N, K // 2), torch.empty((E, N, K // group), dtype=torch.bfloat16, device=device),
+                          u8(E, N, K // group) if zeros else None)
+
+
+@_entry
+def moe_int4_quantize_pack(w, group=128, zeros=True, out=None):
+    """fp32 masters [E, N, K] -> Int4Tensor (with zero points, or symmetric)."""
+    E, N, K = _dims(w, "w", 3)
+    pw = _same(w, "w", w, torch.float32, (E, N, K))
+    if out is None:
+        if group not in (32, 64, 128) or K % 128:
+            raise ValueError(f"group {group} of {K} columns: groups of 32, 64 or 128, columns a multiple of 128")
+        out = Int4Tensor.empty(E, N, K, group, zeros, w.device)
+    if out.shape != (E, N, K):
+        raise ValueError(f"out: shape {out.shape}, expected {(E, N, K)}")
+    st = out.cstruct(w)
+    _check(lib().moe_int4_quantize_pack(pw, ctypes.byref(st), _here()), "moe_int4_quantize_pack")
+    return out
+
+
+@_entry
+def moe_int4_dequantize(t, out=None):
+    """Int4Tensor -> fp32 [E, N, K]."""
+    st = t.cstruct()
+    out = _new(out, "out", t.codes, torch.float32, t.shape)
+    _check(lib().moe_int4_dequantize(ctypes.byref(st), out.data_ptr(), _here()), "moe_int4_dequantize")
+    return out
+
+
+@_entry
+def moe_int4_linear(x, w, offsets=None, sorted_slots=None, k=1, out=None):
+    """bf16 rows times a 4-bit integer projection: x [X, K], w an Int4Tensor.
+    Without offsets a dense projection (E = 1); with them rows by expert, as
+    in moe_grouped_linear.  Returns [M, N] in x's dtype."""
+    X, K = _dims(x, "x", 2)
+    px = _same(x, "x", x, _BITS16, (X, K))
+    if not isinstance(w, Int4Tensor):
+        raise ValueError(f"w: expected an Int4Tensor, got {type(w).__name__}")
+    st = w.cstruct(x)
+    if st.K != K:
+        raise ValueError(f"w: {st.K} columns, x has {K}")
+    po = None if offsets is None else _same(offsets, "offsets", x, torch.int32, (st.E + 1,))
+    M, ps = _rows(x, sorted_slots)
+    out = _new(out, "out", x, x.dtype, (M, st.N))
+    _check(lib().moe_int4_linear(px, X, ctypes.byref(st), po, ps, k, M, out.data_ptr(), _here()), "moe_int4_linear")
+    return out
+
+
+def _tokens(slot_pos, like, k):
+    n, = _dims(slot_pos, "slot_pos", 1)
+    if k < 1 or n % k:
+        raise ValueError(f"slot_pos: {n} entries, not a multiple of k = {k}")
+    return n // k, _same(slot_pos, "slot_pos", like, torch.int32, (n,))
+
+
+@_entry
+def moe_combine(y, slot_pos, k, w=None, out=None):
+    """out[t] = sum_j w[t, j] * y[slot_pos[t * k + j]]: y [M, H] rows by
+    expert, w fp32 [T, k] (None: all 1) -> [T, H] in y's dtype."""
+    M, H = _dims(y, "y", 2)
+    py = _same(y, "y", y, _BITS16, (M, H))
+    T, pp = _tokens(slot_pos, y, k)
+    pw = None if w is None else _same(w, "w", y, torch.float32, (T, k))
+    out = _new(out, "out", y, y.dtype, (T, H))
+    _check(lib().moe_combine(py, M, H, pp, pw, T, k, out.data_ptr(), _here()), "moe_combine")
+    return out
+
+
+@_entry
+def moe_combine_backward(dout, y, slot_pos, w, ids=None, E=0, dy=None, dw=None, dlogits=None):
+    """Gradients of moe_combine: (dy [M, H] in dout's dtype, dw fp32 [T, k]),
+    and with ids (int32 [T, k]) and E the router logits' gradient through the
+    softmax over the k selected: (dy, dw, dlogits fp32 [T, E]).  Rows of dy
+    that slot_pos does not name are not written."""
+    (T, H), (M, _), (_, k) = _dims(dout, "dout", 2), _dims(y, "y", 2), _dims(w, "w", 2)
+    pd, py = _same(dout, "dout", dout, _BITS16, (T, H)), _same(y, "y", dout, _BITS16, (M, H))
+    pp = _same(slot_pos, "slot_pos", dout, torch.int32, (T * k,))
+    pw = _same(w, "w", dout, torch.float32, (T, k))
+    dy, dw = _new(dy, "dy", dout, dout.dtype, (M, H)), _new(dw, "dw", dout, torch.float32, (T, k))
+    pi = pl = None
+    if ids is not None:
+        pi = _same(ids, "ids", dout, torch.int32, (T, k))
+        dlogits = _new(dlogits, "dlogits", dout, torch.float32, (T, E))
+        pl = dlogits.data_ptr()
+    _check(lib().moe_combine_backward(pd, T, H, py, M, pp, pw, pi, k, E, dy.data_ptr(), dw.data_ptr(), pl, _here()),
+           "moe_combine_backward")
+    return (dy, dw) if ids is None else (dy, dw, dlogits)

@@ -33,8 +33,9 @@ COMMON = [
     "-Wall", "-Wno-unused-function", "-Wno-unused-command-line-argument",
     f"-I{INCLUDE}", f"-I{CSRC}",
 ]
-SOURCES = ["abi.cpp", "quantize.hip", "route.hip", "moe_decode.hip", "moe_prefill.hip", "moe_prefill_pipe.hip",
-           "router.hip", "noalloc.hip", "probe.hip"]
+HOST_SOURCES = ["abi.cpp", "abi_experts.cpp"]       # argument checks and dispatch, no device code
+SOURCES = [*HOST_SOURCES, "quantize.hip", "route.hip", "moe_decode.hip", "moe_prefill.hip", "moe_prefill_pipe.hip",
+           "router.hip", "noalloc.hip", "probe.hip", "grouped_mm.hip", "int4.hip", "combine.hip"]
 
 
 def _compile(src, verbose):
@@ -81,20 +82,22 @@ def asan_runtime():
 
 def build_asan():
     """A copy of the library whose host code -- the C ABI's argument checking
-    and dispatch, abi.cpp, which holds no device code -- is compiled as plain
-    C++ by the host compiler with AddressSanitizer; every other object is the
-    normal build's.  For the CPU tests of the C ABI under ASan (the runtime is
-    preloaded into that test's process).  Returns its path."""
+    and dispatch, HOST_SOURCES, which hold no device code -- is compiled as
+    plain C++ by the host compiler with AddressSanitizer; every other object is
+    the normal build's.  For the CPU tests of the C ABI under ASan (the runtime
+    is preloaded into that test's process).  Returns its path."""
     if not all(os.path.exists(os.path.join(BUILD, os.path.splitext(s)[0] + ".o")) for s in SOURCES):
         build()
-    obj = os.path.join(BUILD, "abi_asan.o")
-    cmd = [CLANGXX, "-std=c++17", "-O1", "-fPIC", "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include", f"-I{INCLUDE}",
-           f"-I{CSRC}", "-fsanitize=address", "-fno-omit-frame-pointer", "-c", os.path.join(CSRC, "abi.cpp"),
-           "-o", obj]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"clang++ (ASan) failed for abi.cpp:\n{r.stderr}")
-    objs = [obj] + [os.path.join(BUILD, os.path.splitext(s)[0] + ".o") for s in SOURCES if s != "abi.cpp"]
+    objs = [os.path.join(BUILD, os.path.splitext(s)[0] + ".o") for s in SOURCES if s not in HOST_SOURCES]
+    for src in HOST_SOURCES:
+        obj = os.path.join(BUILD, os.path.splitext(src)[0] + "_asan.o")
+        cmd = [CLANGXX, "-std=c++17", "-O1", "-fPIC", "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include", f"-I{INCLUDE}",
+               f"-I{CSRC}", "-fsanitize=address", "-fno-omit-frame-pointer", "-c", os.path.join(CSRC, src),
+               "-o", obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"clang++ (ASan) failed for {src}:\n{r.stderr}")
+        objs.append(obj)
     r = subprocess.run([HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", ASAN_LIB],
                        capture_output=True, text=True)
     if r.returncode != 0:

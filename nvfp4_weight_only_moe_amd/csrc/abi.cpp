@@ -13,15 +13,13 @@
 #include <string>
 #include <vector>
 
+#include "abi_common.h"
 #include "internal.h"
 
 namespace moe {
 namespace {
 
 constexpr size_t kAlign = 256;
-
-inline size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 moe_status check_tensor(const moe_nvfp4_tensor* t, int E, int N, int K) {
     if (!t || !t->codes || !t->scales || !t->global_scale) return MOE_ERR_INVALID_ARG;
@@ -35,11 +33,6 @@ moe_status check_tensor_self(const moe_nvfp4_tensor* t) {
     if (t->E < 1 || t->N < 1 || t->K < 32 || t->K % 32) return MOE_ERR_SHAPE;
     if (t->E > MOE_MAX_EXPERTS) return MOE_ERR_UNSUPPORTED;
     return check_tensor(t, t->E, t->N, t->K);
-}
-
-bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
 }
 
 // ---- profiling state (benchmarks only)

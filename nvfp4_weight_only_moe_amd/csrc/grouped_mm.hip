@@ -1,0 +1,556 @@
+// Matrix products of bf16 expert weights over expert-sorted rows: the product,
+// the gate/up pair with SwiGLU, the input gradients and the weight gradient.
+//
+// With rows p of expert e = the e-th run of d_offsets, all sums in fp32 on
+// v_mfma_f32_16x16x32_bf16:
+//   k_rows_mm<NT>   y[p][n]  = sum_k x[src(p)][k] W[e][n][k]
+//   k_rows_mm<NN>   dx[p][k] = sum_n dy[p][n] W[e][n][k]   (and a second pair)
+//   k_wgrad         dW[e][n][k] = sum_{p in e} dy[p][n] x[src(p)][k]
+//
+// An operand's tile of one stage (64 steps of the reduction) goes from memory
+// straight to LDS (buffer loads with the LDS as destination: 16 bytes a lane,
+// lanes outside the matrix get an offset past the descriptor and read zeros).
+// Two layouts, by how the operand lies in memory:
+//   reduction contiguous ("RC"): LDS rows of 64 values (128 bytes); 16-byte
+//     unit u of row r sits at unit u ^ (r >> 1 & 7), so the 16 rows of a
+//     fragment read hit 16 different 16-byte bank groups;
+//   reduction outermost ("RO"): LDS rows of 256 output positions (512 bytes),
+//     read through the LDS transpose load (4 x 16 blocks); 32-byte chunk c of
+//     row r sits at chunk c ^ (r & 3 | r >> 1 & 4), so the eight rows that
+//     half a wave reads hit eight different 32-byte bank groups.
+// The output position that is contiguous in memory is the A operand of the
+// MFMA: a lane then holds four neighbouring outputs of one row.
+#include "device_common.h"
+#include "internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 512;             // 8 waves: 2 along the rows x 4 along the columns
+constexpr int kWaves = kThreads / kWave;
+constexpr int kBN = 256;                  // output columns per tile, 64 per wave
+constexpr int kNI = 4;                    // 16-column subtiles per wave
+constexpr int kBK = 64;                   // reduction steps per stage
+constexpr int kStages = 2;                // LDS buffers
+constexpr uint32_t kOutside = 0xFFFFFFFFu;
+constexpr uint32_t kRecords = 0xFFFFFF00u;   // descriptor size: every real offset is below it
+constexpr int kColBytes = kBN * kBK * 2;
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+enum Form { kNT = 0, kNN = 1 };
+enum Epilogue { kPlain = 0, kSwiglu = 1 };
+
+// 16 bytes per lane from (base + voff) to LDS at ldst + 16 * lane; lanes whose
+// voff lies outside the descriptor write zeros.  Inline assembly for the same
+// reason as lds_dma16: the compiler would wait for it before every LDS read.
+__device__ __forceinline__ void lds_dma16_buf(const void* base, uint32_t voff, uint32_t ldst) {
+    const uint64_t b = reinterpret_cast<uint64_t>(base);
+    u32x4 rsrc;
+    rsrc[0] = (uint32_t)b;
+    rsrc[1] = (uint32_t)(b >> 32) & 0xFFFFu;
+    rsrc[2] = kRecords;
+    rsrc[3] = 0x00020000u;
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(rsrc), "{m0}"(ldst) : "memory");
+}
+
+__device__ __forceinline__ const uint16_t* uniform_ptr(const uint16_t* p) {
+    const uint64_t b = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)b), hi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
+    return reinterpret_cast<const uint16_t*>(((uint64_t)hi << 32) | lo);
+}
+
+// slot / k for 0 <= slot < 2^31, with magic = floor(2^32 / k) (k > 1) or 0
+// (k == 1): the estimate is at most one too small.
+__device__ __forceinline__ int slot_token(int slot, int k, uint32_t magic) {
+    if (magic == 0) return slot;
+    uint32_t q = __umulhi((uint32_t)slot, magic);
+    if ((uint32_t)slot - q * (uint32_t)k >= (uint32_t)k) ++q;
+    return (int)q;
+}
+
+struct MmParams {
+    const uint16_t* a0;           // row operand: x, or dy
+    const uint16_t* a1;           // NN: the second pair's dy, or null
+    const uint16_t* w0;           // weights (kSwiglu on NT: gate)
+    const uint16_t* w1;           // kSwiglu on NT: up; NN: the second pair's weights, or null
+    const int32_t* offsets;
+    const int32_t* slots;         // NT: sorted slots, or null (row p is x's row p)
+    int E, M, X, k;
+    uint32_t kmagic;
+    int R, C;                     // reduction length, output columns
+    int pairs;
+    uint16_t *o0, *o1, *o2;       // y | h, a, b | dx | da, db
+    const uint16_t *i0, *i1;      // kSwiglu on NN: the saved a, b
+    int ntc;                      // column tiles
+};
+
+struct RowTile {
+    int e, p0, rows, ct;          // expert (-1: none), first row, rows of the tile, column tile
+};
+
+constexpr int kMGroup = 8;        // row tiles that run beside each other, sharing weight columns in L2
+
+// Tile of workgroup `bid`: the tiles are numbered expert by expert and the
+// eight XCDs take contiguous runs of the numbers (workgroups go to the XCDs
+// in turn).  Offsets are clamped to [0, M], so no tile leaves the buffers.
+template <int BM>
+__device__ __forceinline__ RowTile find_tile(const MmParams& P, int bid) {
+    const int lane = threadIdx.x & 63;
+    const int per = (P.E + kWave - 1) / kWave, b = lane * per;
+    int local = 0;
+    for (int i = 0; i < per; ++i)
+        if (b + i < P.E) {
+            const int lo = max(P.offsets[b + i], 0), hi = min(P.offsets[b + i + 1], P.M);
+            local += (max(hi - lo, 0) + BM - 1) / BM * P.ntc;
+        }
+    const int incl = wave_inclusive_scan_dpp(local);
+    const int total = __builtin_amdgcn_readlane(incl, 63);
+    const int chunk = (total + 7) >> 3, idx = bid >> 3;
+    const int t = (bid & 7) * chunk + idx;
+    RowTile d{-1, 0, 0, 0};
+    if (idx >= chunk || t >= total) return d;
+    const int src = __ffsll((unsigned long long)__ballot(incl > t)) - 1;
+    int first = __builtin_amdgcn_readlane(incl - local, src);
+    for (int i = 0; i < per; ++i) {
+        const int e = src * per + i;
+        const int lo = max(P.offsets[e], 0), hi = min(P.offsets[e + 1], P.M);
+        const int n = max(hi - lo, 0), mt = (n + BM - 1) / BM, tiles = mt * P.ntc;
+        if (t >= first + tiles) {
+            first += tiles;
+            continue;
+        }
+        const int L = t - first, full = mt / kMGroup * kMGroup;
+        int m, c;
+        if (L < full * P.ntc) {
+            const int g = L / (kMGroup * P.ntc), r = L % (kMGroup * P.ntc);
+            c = r / kMGroup;
+            m = g * kMGroup + r % kMGroup;
+        } else {
+            const int r = L - full * P.ntc, last = mt - full;
+            c = r / last;
+            m = full + r % last;
+        }
+        d.e = __builtin_amdgcn_readfirstlane(e);
+        d.p0 = __builtin_amdgcn_readfirstlane(lo + m * BM);
+        d.rows = __builtin_amdgcn_readfirstlane(min(BM, n - m * BM));
+        d.ct = __builtin_amdgcn_readfirstlane(c);
+        return d;
+    }
+    return d;
+}
+
+// ---- fragments: lane l holds output position l & 15, reduction steps
+// 8 (l >> 4) .. + 7 of the k-step
+__device__ __forceinline__ bf16x8 frag_rc(const lds_u8* tile, int lane_off, int sub) {
+    return *reinterpret_cast<const __attribute__((address_space(3))) bf16x8*>(tile + lane_off + sub * 2048);
+}
+__device__ __forceinline__ bf16x8 frag_ro(const lds_u8* tile, int lane_off) {
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + lane_off));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + lane_off + 4 * 512));
+    typedef short s16x8 __attribute__((ext_vector_type(8)));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+__device__ __forceinline__ int ro_swizzle(int row) { return (row & 3) | ((row >> 1) & 4); }
+
+__device__ __forceinline__ uint32_t pack_rne(float lo, float hi) {
+    return (uint32_t)f32_to_bf16_rne(lo) | ((uint32_t)f32_to_bf16_rne(hi) << 16);
+}
+__device__ __forceinline__ void store4(uint16_t* p, floatx4 v) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_rne(v[0], v[1]), pack_rne(v[2], v[3]));
+}
+__device__ __forceinline__ floatx4 load4(const uint16_t* p) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    return floatx4{bf16_bits_to_f32(u.x & 0xFFFFu), bf16_bits_to_f32(u.x >> 16), bf16_bits_to_f32(u.y & 0xFFFFu),
+                   bf16_bits_to_f32(u.y >> 16)};
+}
+
+template <int FORM, int EPI, int BM>
+__global__ void __launch_bounds__(kThreads) k_rows_mm(MmParams P) {
+    constexpr int MI = BM / 32;                     // 16-row subtiles per wave
+    constexpr int kRowBytes = BM * kBK * 2;
+    constexpr int kStageBytes = kRowBytes + kColBytes;
+    constexpr int kADma = kRowBytes / 1024 / kWaves, kBDma = kColBytes / 1024 / kWaves;
+    constexpr bool kGateUp = FORM == kNT && EPI == kSwiglu;   // 128 gate + 128 up columns per tile
+    constexpr int kTileCols = kGateUp ? kBN / 2 : kBN;        // output columns per tile
+    extern __shared__ __align__(16) uint8_t smem[];
+
+    const RowTile t = find_tile<BM>(P, blockIdx.x);
+    if (t.e < 0) return;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave >> 2, wn = wave & 3;
+    const int lrow = lane & 15, q = lane >> 4;
+    const int c0 = t.ct * kTileCols;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_u8*)smem;
+
+    // row operand: per-lane byte offset of its rows (one per DMA)
+    uint32_t aoff[kADma];
+    int aunit[kADma];
+    const int64_t abase = P.slots ? 0 : (int64_t)t.p0 * P.R;
+#pragma unroll
+    for (int i = 0; i < kADma; ++i) {
+        const int r = (i * kWaves + wave) * 8 + (lane >> 3);
+        aunit[i] = (lane & 7) ^ ((r >> 1) & 7);
+        int src = r;
+        bool ok = r < t.rows;
+        if (P.slots && ok) {
+            const int slot = P.slots[t.p0 + r];
+            src = slot_token(slot, P.k, P.kmagic);
+            ok = slot >= 0 && src < P.X;
+        }
+        aoff[i] = ok ? (uint32_t)src * (uint32_t)P.R * 2u + aunit[i] * 16 : kOutside;
+    }
+    // column operand
+    uint32_t boff[kBDma];
+    int bpos[kBDma];                                // RC: unit; RO: reduction row inside the stage
+    const int64_t wbase = FORM == kNT ? ((int64_t)t.e * P.C + c0) * P.R : (int64_t)t.e * P.R * P.C + c0;
+#pragma unroll
+    for (int i = 0; i < kBDma; ++i) {
+        if constexpr (FORM == kNT) {
+            const int r = (i * kWaves + wave) * 8 + (lane >> 3);
+            const int n = kGateUp ? r & (kBN / 2 - 1) : r;
+            bpos[i] = (lane & 7) ^ ((r >> 1) & 7);
+            boff[i] = c0 + n < P.C ? (uint32_t)n * (uint32_t)P.R * 2u + bpos[i] * 16 : kOutside;
+        } else {
+            const int r = (i * kWaves + wave) * 2 + (lane >> 5);
+            const int pos = lane & 31, col = (((pos >> 1) ^ ro_swizzle(r)) << 4) + ((pos & 1) << 3);
+            bpos[i] = r;
+            boff[i] = c0 + col < P.C ? (uint32_t)r * (uint32_t)P.C * 2u + col * 2 : kOutside;
+        }
+    }
+
+    const int spp = (P.R + kBK - 1) / kBK;          // stages per pair
+    const int nstages = spp * P.pairs;
+    const auto dma = [&](int s) {
+        const int pair = FORM == kNN && s >= spp ? 1 : 0;
+        const int r0 = (s - pair * spp) * kBK;
+        const uint16_t* a = uniform_ptr((pair ? P.a1 : P.a0) + abase + r0);
+        const uint32_t buf = lds0 + (s % kStages) * kStageBytes;
+#pragma unroll
+        for (int i = 0; i < kADma; ++i) {
+            const uint32_t vo = r0 + aunit[i] * 8 < P.R ? aoff[i] : kOutside;
+            lds_dma16_buf(a, vo, buf + (i * kWaves + wave) * 1024);
+        }
+#pragma unroll
+        for (int i = 0; i < kBDma; ++i) {
+            const bool up = kGateUp && i >= kBDma / 2;
+            const uint16_t* w = uniform_ptr((pair || up ? P.w1 : P.w0) + wbase + (FORM == kNT ? (int64_t)r0 : (int64_t)r0 * P.C));
+            const bool ok = FORM == kNT ? r0 + bpos[i] * 8 < P.R : r0 + bpos[i] < P.R;
+            lds_dma16_buf(w, ok ? boff[i] : kOutside, buf + kRowBytes + (i * kWaves + wave) * 1024);
+        }
+    };
+
+    // lane offsets of the fragments
+    int aread[2], bread[2], bchunk[kNI];
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+        const int u = ((ks * 4 + q) ^ (lrow >> 1)) * 16;
+        aread[ks] = (wm * (BM / 2) + lrow) * 128 + u;
+        if constexpr (FORM == kNT)
+            bread[ks] = ((kGateUp ? wn * 32 : wn * 64) + lrow) * 128 + u;
+        else
+            bread[ks] = (ks * 32 + q * 8 + (lrow >> 2)) * 512 + (lrow & 3) * 8;
+    }
+    const int bsw = (lrow >> 2) | ((q & 1) << 2);   // ro_swizzle of the lane's rows
+#pragma unroll
+    for (int ni = 0; ni < kNI; ++ni) bchunk[ni] = ((wn * 4 + ni) ^ bsw) * 32;
+
+    floatx4 acc[MI][kNI];
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int ni = 0; ni < kNI; ++ni) acc[mi][ni] = floatx4{0, 0, 0, 0};
+
+    dma(0);
+    for (int s = 0; s < nstages; ++s) {
+        wait_vmem_at_most<0>();                     // stage s is in LDS (this wave's part) ...
+        wait_lds_barrier();                         // ... and everybody's; the other buffer is no longer read
+        if (s + 1 < nstages) dma(s + 1);
+        const lds_u8* as = (const lds_u8*)smem + (s % kStages) * kStageBytes;
+        const lds_u8* bs = as + kRowBytes;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            bf16x8 af[MI], bf[kNI];
+#pragma unroll
+            for (int ni = 0; ni < kNI; ++ni) {
+                if constexpr (FORM == kNT)
+                    bf[ni] = frag_rc(bs, bread[ks], kGateUp && ni >= 2 ? ni + 6 : ni);
+                else
+                    bf[ni] = frag_ro(bs, bread[ks] + bchunk[ni]);
+            }
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi) af[mi] = frag_rc(as, aread[ks], mi);
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+                for (int ni = 0; ni < kNI; ++ni)
+                    acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[ni], af[mi], acc[mi][ni], 0, 0, 0);
+        }
+    }
+
+    // one rounding to bf16 per output
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+        const int r = wm * (BM / 2) + mi * 16 + lrow;
+        if (r >= t.rows) continue;
+        const int64_t row = (int64_t)(t.p0 + r) * P.C;
+#pragma unroll
+        for (int ni = 0; ni < (kGateUp ? 2 : kNI); ++ni) {
+            const int c = c0 + (kGateUp ? wn * 32 : wn * 64) + ni * 16 + q * 4;
+            if (c >= P.C) continue;
+            if constexpr (kGateUp) {
+                const floatx4 a = acc[mi][ni], b = acc[mi][ni + 2];
+                floatx4 h;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h[i] = silu(a[i]) * b[i];
+                store4(P.o0 + row + c, h);
+                if (P.o1) {
+                    store4(P.o1 + row + c, a);
+                    store4(P.o2 + row + c, b);
+                }
+            } else if constexpr (EPI == kSwiglu) {
+                // dh = acc; da = dh b s (1 + a (1 - s)), db = dh a s, s = sigmoid(a)
+                const floatx4 a = load4(P.i0 + row + c), b = load4(P.i1 + row + c), dh = acc[mi][ni];
+                floatx4 da, db;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float sg = 1.0f / (1.0f + __expf(-a[i]));
+                    db[i] = dh[i] * a[i] * sg;
+                    da[i] = dh[i] * b[i] * (sg + a[i] * sg * (1.0f - sg));
+                }
+                store4(P.o0 + row + c, da);
+                store4(P.o1 + row + c, db);
+            } else {
+                store4(P.o0 + row + c, acc[mi][ni]);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- weight gradient
+struct WgradParams {
+    const uint16_t* dy;           // [M][N]
+    const uint16_t* x;            // [X][K]
+    const int32_t* offsets;
+    const int32_t* slots;
+    int E, M, X, k;
+    uint32_t kmagic;
+    int N, K, ntn, ntk;
+    int accumulate;
+    float* dw;                    // [E][N][K]
+};
+
+constexpr int kWM = 256;          // rows n of a wgrad tile
+
+__global__ void __launch_bounds__(kThreads) k_wgrad(WgradParams P) {
+    constexpr int MI = kWM / 32, kDma = 4;
+    constexpr int kStageBytes = 2 * kColBytes;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int per_e = P.ntn * P.ntk;
+    // the XCDs take contiguous runs of tiles
+    const int total = P.E * per_e, chunk = (total + 7) >> 3, idx = blockIdx.x >> 3;
+    const int tile = (blockIdx.x & 7) * chunk + idx;
+    if (idx >= chunk || tile >= total) return;
+    const int e = tile / per_e, n0 = tile % per_e % P.ntn * kWM, k0 = tile % per_e / P.ntn * kBN;
+    const int p0 = max(P.offsets[e], 0), cnt = max(min(P.offsets[e + 1], P.M) - p0, 0);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave >> 2, wn = wave & 3;
+    const int lrow = lane & 15, q = lane >> 4;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_u8*)smem;
+
+    uint32_t aoff[kDma], xcol[kDma];
+    int rr[kDma], slot[kDma];
+#pragma unroll
+    for (int i = 0; i < kDma; ++i) {
+        const int r = (i * kWaves + wave) * 2 + (lane >> 5);
+        const int pos = lane & 31, col = (((pos >> 1) ^ ro_swizzle(r)) << 4) + ((pos & 1) << 3);
+        rr[i] = r;
+        aoff[i] = n0 + col < P.N ? (uint32_t)r * (uint32_t)P.N * 2u + col * 2 : kOutside;
+        xcol[i] = k0 + col < P.K ? (uint32_t)col * 2u : kOutside;
+        slot[i] = 0;
+    }
+    const int nstages = (cnt + kBK - 1) / kBK;
+    const auto load_slots = [&](int s) {
+        if (!P.slots) return;
+#pragma unroll
+        for (int i = 0; i < kDma; ++i) slot[i] = P.slots[min(p0 + s * kBK + rr[i], P.M - 1)];
+    };
+    const auto dma = [&](int s) {
+        const int r0 = s * kBK;
+        const uint32_t buf = lds0 + (s % kStages) * kStageBytes;
+        const uint16_t* a = uniform_ptr(P.dy + (int64_t)(p0 + r0) * P.N + n0);
+        const uint16_t* x = uniform_ptr(P.x + (P.slots ? 0 : (int64_t)(p0 + r0) * P.K) + k0);
+#pragma unroll
+        for (int i = 0; i < kDma; ++i)
+            lds_dma16_buf(a, r0 + rr[i] < cnt ? aoff[i] : kOutside, buf + (i * kWaves + wave) * 1024);
+#pragma unroll
+        for (int i = 0; i < kDma; ++i) {
+            int src = rr[i];
+            bool ok = r0 + rr[i] < cnt && xcol[i] != kOutside;
+            if (P.slots) {
+                src = slot_token(slot[i], P.k, P.kmagic);
+                ok = ok && slot[i] >= 0 && src < P.X;
+            }
+            lds_dma16_buf(x, ok ? (uint32_t)src * (uint32_t)P.K * 2u + xcol[i] : kOutside,
+                          buf + kColBytes + (i * kWaves + wave) * 1024);
+        }
+    };
+
+    int rd[2], ac[MI], bc[kNI];
+    const int sw = (lrow >> 2) | ((q & 1) << 2);
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) rd[ks] = (ks * 32 + q * 8 + (lrow >> 2)) * 512 + (lrow & 3) * 8;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) ac[mi] = ((wm * 8 + mi) ^ sw) * 32;
+#pragma unroll
+    for (int ni = 0; ni < kNI; ++ni) bc[ni] = ((wn * 4 + ni) ^ sw) * 32;
+
+    floatx4 acc[MI][kNI];
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int ni = 0; ni < kNI; ++ni) acc[mi][ni] = floatx4{0, 0, 0, 0};
+
+    if (nstages > 0) {
+        load_slots(0);
+        dma(0);
+        load_slots(1);
+    }
+    for (int s = 0; s < nstages; ++s) {
+        wait_vmem_at_most<0>();
+        wait_lds_barrier();
+        if (s + 1 < nstages) {
+            dma(s + 1);
+            load_slots(s + 2);
+        }
+        const lds_u8* as = (const lds_u8*)smem + (s % kStages) * kStageBytes;
+        const lds_u8* bs = as + kColBytes;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            bf16x8 af[MI], bf[kNI];
+#pragma unroll
+            for (int ni = 0; ni < kNI; ++ni) bf[ni] = frag_ro(bs, rd[ks] + bc[ni]);
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi) af[mi] = frag_ro(as, rd[ks] + ac[mi]);
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+                for (int ni = 0; ni < kNI; ++ni)
+                    acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[ni], af[mi], acc[mi][ni], 0, 0, 0);
+        }
+    }
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+        const int n = n0 + wm * 128 + mi * 16 + lrow;
+        if (n >= P.N) continue;
+        float* row = P.dw + ((int64_t)e * P.N + n) * P.K;
+#pragma unroll
+        for (int ni = 0; ni < kNI; ++ni) {
+            const int c = k0 + wn * 64 + ni * 16 + q * 4;
+            if (c >= P.K) continue;
+            floatx4 v = acc[mi][ni];
+            if (P.accumulate) v += *reinterpret_cast<const floatx4*>(row + c);
+            *reinterpret_cast<floatx4*>(row + c) = v;
+        }
+    }
+}
+
+uint32_t div_magic(int k) { return k <= 1 ? 0u : (uint32_t)((1ull << 32) / (uint32_t)k); }
+
+// Workgroups of a row-tiled launch: at most floor(M / BM) + min(E, M) row
+// tiles exist (one partial tile per expert); the ones beyond leave at once.
+int64_t row_tiles_bound(int M, int E, int BM) { return M / BM + (int64_t)std::min(E, M); }
+
+template <int FORM, int EPI, int BM>
+moe_status launch_rows(const MmParams& P, const char* name, hipStream_t s) {
+    const int64_t grid = (row_tiles_bound(P.M, P.E, BM) * P.ntc + 7) / 8 * 8;
+    const size_t lds = kStages * (BM * kBK * 2 + kColBytes);
+    moe_status st = allow_dynamic_lds(reinterpret_cast<const void*>(&k_rows_mm<FORM, EPI, BM>), lds);
+    if (st != MOE_OK) return st;
+    MOE_LAUNCH(name, (k_rows_mm<FORM, EPI, BM>), dim3((unsigned)grid), dim3(kThreads), lds, s, P);
+    return MOE_OK;
+}
+
+template <int FORM, int EPI>
+moe_status launch_rows_any(const MmParams& P, const char* name, hipStream_t s) {
+    const int64_t mean = P.M / std::max(1, std::min(P.E, P.M));
+    if (mean > 128) return launch_rows<FORM, EPI, 256>(P, name, s);
+    if (mean > 48) return launch_rows<FORM, EPI, 128>(P, name, s);
+    return launch_rows<FORM, EPI, 64>(P, name, s);
+}
+
+}  // namespace
+
+bool grouped_grid_fits(int M, int E, int C) {
+    return (M / 64 + (int64_t)std::min(E, M)) * ((C + 127) / 128) < (1 << 22);
+}
+
+moe_status launch_grouped_fwd(const GroupedArgs& g, hipStream_t s) {
+    MmParams P{};
+    P.a0 = g.x;
+    P.w0 = g.w;
+    P.w1 = g.w2;
+    P.offsets = g.offsets;
+    P.slots = g.slots;
+    P.E = g.E; P.M = g.M; P.X = g.X; P.k = g.k;
+    P.kmagic = div_magic(g.k);
+    P.R = g.K; P.C = g.N;
+    P.pairs = 1;
+    P.o0 = g.o0; P.o1 = g.o1; P.o2 = g.o2;
+    if (g.w2) {
+        P.ntc = (g.N + kBN / 2 - 1) / (kBN / 2);
+        return launch_rows_any<kNT, kSwiglu>(P, "grouped_swiglu", s);
+    }
+    P.ntc = (g.N + kBN - 1) / kBN;
+    return launch_rows_any<kNT, kPlain>(P, "grouped_linear", s);
+}
+
+moe_status launch_grouped_dgrad(const GroupedArgs& g, hipStream_t s) {
+    MmParams P{};
+    P.a0 = g.dy;
+    P.a1 = g.dy2;
+    P.w0 = g.w;
+    P.w1 = g.w2;
+    P.offsets = g.offsets;
+    P.E = g.E; P.M = g.M; P.X = g.M; P.k = 1;
+    P.R = g.N; P.C = g.K;
+    P.pairs = g.dy2 ? 2 : 1;
+    P.o0 = g.o0; P.o1 = g.o1;
+    P.i0 = g.a; P.i1 = g.b;
+    P.ntc = (g.K + kBN - 1) / kBN;
+    if (g.a) return launch_rows_any<kNN, kSwiglu>(P, "grouped_swiglu_dgrad", s);
+    return launch_rows_any<kNN, kPlain>(P, "grouped_dgrad", s);
+}
+
+size_t grouped_wgrad_workspace_bytes(int M, int N, int K, int E) {
+    (void)M; (void)N; (void)K; (void)E;
+    return 0;
+}
+
+moe_status launch_grouped_wgrad(const GroupedArgs& g, float* dw, bool accumulate, void* ws, hipStream_t s) {
+    (void)ws;
+    WgradParams P{};
+    P.dy = g.dy;
+    P.x = g.x;
+    P.offsets = g.offsets;
+    P.slots = g.slots;
+    P.E = g.E; P.M = g.M; P.X = g.X; P.k = g.k;
+    P.kmagic = div_magic(g.k);
+    P.N = g.N; P.K = g.K;
+    P.ntn = (g.N + kWM - 1) / kWM;
+    P.ntk = (g.K + kBN - 1) / kBN;
+    P.accumulate = accumulate;
+    P.dw = dw;
+    const int64_t grid = ((int64_t)g.E * P.ntn * P.ntk + 7) / 8 * 8;
+    const size_t lds = kStages * 2 * kColBytes;
+    moe_status st = allow_dynamic_lds(reinterpret_cast<const void*>(&k_wgrad), lds);
+    if (st != MOE_OK) return st;
+    MOE_LAUNCH("grouped_wgrad", k_wgrad, dim3((unsigned)grid), dim3(kThreads), lds, s, P);
+    return MOE_OK;
+}
+
+}  // namespace moe

@@ -129,4 +129,34 @@ bool prefill_pipe_supported(int64_t T, int k, int H, int I);
 moe_status launch_gateup_pipe(const FwdArgs& a, hipStream_t s);
 moe_status launch_down_pipe(const FwdArgs& a, hipStream_t s);
 
+// ---- grouped_mm.hip: products of bf16 expert weights over expert-sorted rows
+struct GroupedArgs {
+    const uint16_t* x;          // [X][K] (forward and weight gradient)
+    const uint16_t *dy, *dy2;   // [M][N] (gradients)
+    const uint16_t *w, *w2;     // [E][N][K]
+    const int32_t* offsets;     // [E + 1]
+    const int32_t* slots;       // [M] sorted slots (row p reads x's row slots[p] / k), or null
+    int E, M, X, k, N, K;
+    const uint16_t *a, *b;      // SwiGLU gradient: the saved gate and up outputs [M][K]
+    uint16_t *o0, *o1, *o2;     // y | h, a, b | dx | da, db
+};
+bool grouped_grid_fits(int M, int E, int C);   // the launch of M rows and C output columns
+moe_status launch_grouped_fwd(const GroupedArgs& g, hipStream_t s);      // w2 set: gate/up with SwiGLU
+moe_status launch_grouped_dgrad(const GroupedArgs& g, hipStream_t s);    // a set: through SwiGLU
+size_t grouped_wgrad_workspace_bytes(int M, int N, int K, int E);
+moe_status launch_grouped_wgrad(const GroupedArgs& g, float* dw, bool accumulate, void* ws, hipStream_t s);
+
+// ---- int4.hip: 4-bit integer weights
+moe_status launch_int4_pack(const float* w, const moe_int4_tensor* t, hipStream_t s);
+moe_status launch_int4_dequant(const moe_int4_tensor* t, float* out, hipStream_t s);
+moe_status launch_int4_linear(const uint16_t* x, int X, const moe_int4_tensor* t, const int32_t* offsets,
+                              const int32_t* slots, int k, int M, uint16_t* out, hipStream_t s);
+
+// ---- combine.hip
+moe_status launch_combine_rows(const uint16_t* y, int M, int H, const int32_t* pos, const float* w, int T, int k,
+                               uint16_t* out, hipStream_t s);
+moe_status launch_combine_bwd(const uint16_t* dout, const uint16_t* y, const int32_t* pos, const float* w,
+                              const int32_t* ids, int T, int M, int H, int k, int E, uint16_t* dy, float* dw,
+                              float* dlogits, hipStream_t s);
+
 }  // namespace moe
