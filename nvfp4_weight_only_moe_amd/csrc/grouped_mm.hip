@@ -23,6 +23,8 @@
 #include "device_common.h"
 #include "internal.h"
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
@@ -31,7 +33,9 @@ constexpr int kWaves = kThreads / kWave;
 constexpr int kBN = 256;                  // output columns per tile, 64 per wave
 constexpr int kNI = 4;                    // 16-column subtiles per wave
 constexpr int kBK = 64;                   // reduction steps per stage
-constexpr int kStages = 2;                // LDS buffers
+// LDS buffers of a stage (64 KB with 256 rows, 48 with 128, 40 with 64): what
+// fits 160 KB for one workgroup, with 64 rows for two.
+template <int BM> constexpr int stages() { return BM == 128 ? 3 : 2; }
 constexpr uint32_t kOutside = 0xFFFFFFFFu;
 constexpr uint32_t kRecords = 0xFFFFFF00u;   // descriptor size: every real offset is below it
 constexpr int kColBytes = kBN * kBK * 2;
@@ -71,6 +75,68 @@ __device__ __forceinline__ int slot_token(int slot, int k, uint32_t magic) {
     return (int)q;
 }
 
+// The stages of a tile, through a ring of NS LDS buffers.  Fragments are read
+// one k-step ahead: while the MFMAs of a stage's first half run, its second
+// half is read (in place, a fragment as soon as its four MFMAs are issued);
+// then every wave has read all of the stage, its buffer takes the stage NS
+// later, and the next stage's first half is read under the second half's
+// MFMAs.  OPS: DMAs of a wave per stage, which complete in order.
+template <int NS, int U, int OPS, int READS_A, int READS_B, class Dma, class ReadA, class ReadB, class Acc>
+__device__ __forceinline__ void run_stages(int nstages, Dma&& dma, ReadA&& ra, ReadB&& rb, Acc& acc) {
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+        if (i < nstages) dma(i);
+    if (NS >= 3 && nstages >= 3) wait_vmem_at_most<2 * OPS>();
+    else if (nstages >= 2) wait_vmem_at_most<OPS>();
+    else wait_vmem_at_most<0>();
+    wait_lds_barrier();
+    bf16x8 af[U], b0[kNI], b1[kNI];
+#pragma unroll
+    for (int ni = 0; ni < kNI; ++ni) b0[ni] = rb(0, 0, ni);
+#pragma unroll
+    for (int mi = 0; mi < U; ++mi) af[mi] = ra(0, 0, mi);
+    int buf = 0;
+    for (int s = 0; s < nstages; ++s) {
+#pragma unroll
+        for (int ni = 0; ni < kNI; ++ni) b1[ni] = rb(buf, 1, ni);
+#pragma unroll
+        for (int mi = 0; mi < U; ++mi) {
+#pragma unroll
+            for (int ni = 0; ni < kNI; ++ni)
+                acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b0[ni], af[mi], acc[mi][ni], 0, 0, 0);
+            af[mi] = ra(buf, 1, mi);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x100, kNI * READS_B, 0);
+#pragma unroll
+        for (int mi = 0; mi < U; ++mi) {
+            __builtin_amdgcn_sched_group_barrier(0x008, kNI, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, READS_A, 0);
+        }
+        // stage s + 1 is in LDS (stages behind it may be in flight) and nobody reads stage s any more
+        if (NS >= 3 && s + 2 < nstages) wait_vmem_at_most<OPS>();
+        else wait_vmem_at_most<0>();
+        wait_lds_barrier();
+        if (s + NS < nstages) dma(s + NS);
+        buf = buf + 1 == NS ? 0 : buf + 1;
+        // behind the last stage this reads a buffer whose values nobody uses
+#pragma unroll
+        for (int ni = 0; ni < kNI; ++ni) b0[ni] = rb(buf, 0, ni);
+#pragma unroll
+        for (int mi = 0; mi < U; ++mi) {
+#pragma unroll
+            for (int ni = 0; ni < kNI; ++ni)
+                acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1[ni], af[mi], acc[mi][ni], 0, 0, 0);
+            af[mi] = ra(buf, 0, mi);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x100, kNI * READS_B, 0);
+#pragma unroll
+        for (int mi = 0; mi < U; ++mi) {
+            __builtin_amdgcn_sched_group_barrier(0x008, kNI, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, READS_A, 0);
+        }
+    }
+}
+
 struct MmParams {
     const uint16_t* a0;           // row operand: x, or dy
     const uint16_t* a1;           // NN: the second pair's dy, or null
@@ -93,9 +159,20 @@ struct RowTile {
 
 constexpr int kMGroup = 8;        // row tiles that run beside each other, sharing weight columns in L2
 
-// Tile of workgroup `bid`: the tiles are numbered expert by expert and the
-// eight XCDs take contiguous runs of the numbers (workgroups go to the XCDs
-// in turn).  Offsets are clamped to [0, M], so no tile leaves the buffers.
+// Number of workgroup `bid` among `total` tiles, or -1: the eight XCDs (which
+// the workgroups go to in turn, 32 CUs each) take equal runs of at most 32
+// tiles in turn, so that neighbours meet in one L2, no XCD gets all the long
+// experts and none gets a run more than another.
+__device__ __forceinline__ int xcd_tile(int bid, int total) {
+    const int rounds = max((total + 255) >> 8, 1), run = (total + 8 * rounds - 1) / (8 * rounds), idx = bid >> 3;
+    const int t = ((idx / max(run, 1)) * 8 + (bid & 7)) * run + idx % max(run, 1);
+    return t < total ? t : -1;
+}
+// workgroups that number at most `total` tiles that way
+int64_t xcd_grid(int64_t total) { return total + 8 * ((total + 255) / 256) + 8; }
+
+// Tile of workgroup `bid`: the tiles are numbered expert by expert.  Offsets
+// are clamped to [0, M], so no tile leaves the buffers.
 template <int BM>
 __device__ __forceinline__ RowTile find_tile(const MmParams& P, int bid) {
     const int lane = threadIdx.x & 63;
@@ -108,10 +185,9 @@ __device__ __forceinline__ RowTile find_tile(const MmParams& P, int bid) {
         }
     const int incl = wave_inclusive_scan_dpp(local);
     const int total = __builtin_amdgcn_readlane(incl, 63);
-    const int chunk = (total + 7) >> 3, idx = bid >> 3;
-    const int t = (bid & 7) * chunk + idx;
+    const int t = xcd_tile(bid, total);
     RowTile d{-1, 0, 0, 0};
-    if (idx >= chunk || t >= total) return d;
+    if (t < 0) return d;
     const int src = __ffsll((unsigned long long)__ballot(incl > t)) - 1;
     int first = __builtin_amdgcn_readlane(incl - local, src);
     for (int i = 0; i < per; ++i) {
@@ -150,7 +226,6 @@ __device__ __forceinline__ bf16x8 frag_rc(const lds_u8* tile, int lane_off, int 
 __device__ __forceinline__ bf16x8 frag_ro(const lds_u8* tile, int lane_off) {
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + lane_off));
     const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + lane_off + 4 * 512));
-    typedef short s16x8 __attribute__((ext_vector_type(8)));
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 __device__ __forceinline__ int ro_swizzle(int row) { return (row & 3) | ((row >> 1) & 4); }
@@ -168,8 +243,9 @@ __device__ __forceinline__ floatx4 load4(const uint16_t* p) {
 }
 
 template <int FORM, int EPI, int BM>
-__global__ void __launch_bounds__(kThreads) k_rows_mm(MmParams P) {
+__global__ void __launch_bounds__(kThreads, BM == 64 ? 4 : 2) k_rows_mm(MmParams P) {
     constexpr int MI = BM / 32;                     // 16-row subtiles per wave
+    constexpr int NS = stages<BM>();
     constexpr int kRowBytes = BM * kBK * 2;
     constexpr int kStageBytes = kRowBytes + kColBytes;
     constexpr int kADma = kRowBytes / 1024 / kWaves, kBDma = kColBytes / 1024 / kWaves;
@@ -228,7 +304,7 @@ __global__ void __launch_bounds__(kThreads) k_rows_mm(MmParams P) {
         const int pair = FORM == kNN && s >= spp ? 1 : 0;
         const int r0 = (s - pair * spp) * kBK;
         const uint16_t* a = uniform_ptr((pair ? P.a1 : P.a0) + abase + r0);
-        const uint32_t buf = lds0 + (s % kStages) * kStageBytes;
+        const uint32_t buf = lds0 + (s % NS) * kStageBytes;
 #pragma unroll
         for (int i = 0; i < kADma; ++i) {
             const uint32_t vo = r0 + aunit[i] * 8 < P.R ? aoff[i] : kOutside;
@@ -248,7 +324,7 @@ __global__ void __launch_bounds__(kThreads) k_rows_mm(MmParams P) {
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
         const int u = ((ks * 4 + q) ^ (lrow >> 1)) * 16;
-        aread[ks] = (wm * (BM / 2) + lrow) * 128 + u;
+        aread[ks] = (wm * 16 + lrow) * 128 + u;
         if constexpr (FORM == kNT)
             bread[ks] = ((kGateUp ? wn * 32 : wn * 64) + lrow) * 128 + u;
         else
@@ -264,37 +340,33 @@ __global__ void __launch_bounds__(kThreads) k_rows_mm(MmParams P) {
 #pragma unroll
         for (int ni = 0; ni < kNI; ++ni) acc[mi][ni] = floatx4{0, 0, 0, 0};
 
-    dma(0);
-    for (int s = 0; s < nstages; ++s) {
-        wait_vmem_at_most<0>();                     // stage s is in LDS (this wave's part) ...
-        wait_lds_barrier();                         // ... and everybody's; the other buffer is no longer read
-        if (s + 1 < nstages) dma(s + 1);
-        const lds_u8* as = (const lds_u8*)smem + (s % kStages) * kStageBytes;
-        const lds_u8* bs = as + kRowBytes;
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            bf16x8 af[MI], bf[kNI];
-#pragma unroll
-            for (int ni = 0; ni < kNI; ++ni) {
-                if constexpr (FORM == kNT)
-                    bf[ni] = frag_rc(bs, bread[ks], kGateUp && ni >= 2 ? ni + 6 : ni);
-                else
-                    bf[ni] = frag_ro(bs, bread[ks] + bchunk[ni]);
-            }
-#pragma unroll
-            for (int mi = 0; mi < MI; ++mi) af[mi] = frag_rc(as, aread[ks], mi);
-#pragma unroll
-            for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-                for (int ni = 0; ni < kNI; ++ni)
-                    acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[ni], af[mi], acc[mi][ni], 0, 0, 0);
-        }
-    }
+    // the stages, for the first U of each wave's 16-row subtiles
+    const auto run = [&](auto used) {
+        constexpr int U = decltype(used)::value;
+        run_stages<NS, U, kADma + kBDma, 1, FORM == kNT ? 1 : 2>(
+            nstages, dma,
+            [&](int buf, int ks, int mi) { return frag_rc((const lds_u8*)smem + buf * kStageBytes, aread[ks], 2 * mi); },
+            [&](int buf, int ks, int ni) {
+                const lds_u8* bs = (const lds_u8*)smem + buf * kStageBytes + kRowBytes;
+                if constexpr (FORM == kNT) return frag_rc(bs, bread[ks], kGateUp && ni >= 2 ? ni + 6 : ni);
+                else return frag_ro(bs, bread[ks] + bchunk[ni]);
+            },
+            acc);
+    };
+    // The two waves of a SIMD take the tile's 16-row subtiles in turn, so a
+    // short tile costs both the same; five copies of the loop (1, 2, 4, 6 or 8
+    // subtiles a wave) leave out what lies behind the tile's last row.
+    const int need = (t.rows + 31) >> 5;
+    if (need <= 1) run(std::integral_constant<int, 1>{});
+    else if (MI <= 2 || need <= 2) run(std::integral_constant<int, 2>{});
+    else if (MI <= 4 || need <= 4) run(std::integral_constant<int, (MI < 4 ? MI : 4)>{});
+    else if (need <= 6) run(std::integral_constant<int, (MI < 6 ? MI : 6)>{});
+    else run(std::integral_constant<int, MI>{});
 
     // one rounding to bf16 per output
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
-        const int r = wm * (BM / 2) + mi * 16 + lrow;
+        const int r = mi * 32 + wm * 16 + lrow;
         if (r >= t.rows) continue;
         const int64_t row = (int64_t)(t.p0 + r) * P.C;
 #pragma unroll
@@ -346,14 +418,12 @@ struct WgradParams {
 constexpr int kWM = 256;          // rows n of a wgrad tile
 
 __global__ void __launch_bounds__(kThreads) k_wgrad(WgradParams P) {
-    constexpr int MI = kWM / 32, kDma = 4;
+    constexpr int MI = kWM / 32, kDma = 4, NS = stages<kWM>();
     constexpr int kStageBytes = 2 * kColBytes;
     extern __shared__ __align__(16) uint8_t smem[];
     const int per_e = P.ntn * P.ntk;
-    // the XCDs take contiguous runs of tiles
-    const int total = P.E * per_e, chunk = (total + 7) >> 3, idx = blockIdx.x >> 3;
-    const int tile = (blockIdx.x & 7) * chunk + idx;
-    if (idx >= chunk || tile >= total) return;
+    const int tile = xcd_tile(blockIdx.x, P.E * per_e);
+    if (tile < 0) return;
     const int e = tile / per_e, n0 = tile % per_e % P.ntn * kWM, k0 = tile % per_e / P.ntn * kBN;
     const int p0 = max(P.offsets[e], 0), cnt = max(min(P.offsets[e + 1], P.M) - p0, 0);
     const int lane = threadIdx.x & 63;
@@ -381,7 +451,7 @@ __global__ void __launch_bounds__(kThreads) k_wgrad(WgradParams P) {
     };
     const auto dma = [&](int s) {
         const int r0 = s * kBK;
-        const uint32_t buf = lds0 + (s % kStages) * kStageBytes;
+        const uint32_t buf = lds0 + (s % NS) * kStageBytes;
         const uint16_t* a = uniform_ptr(P.dy + (int64_t)(p0 + r0) * P.N + n0);
         const uint16_t* x = uniform_ptr(P.x + (P.slots ? 0 : (int64_t)(p0 + r0) * P.K) + k0);
 #pragma unroll
@@ -398,6 +468,7 @@ __global__ void __launch_bounds__(kThreads) k_wgrad(WgradParams P) {
             lds_dma16_buf(x, ok ? (uint32_t)src * (uint32_t)P.K * 2u + xcol[i] : kOutside,
                           buf + kColBytes + (i * kWaves + wave) * 1024);
         }
+        load_slots(s + 1);                          // for the next call
     };
 
     int rd[2], ac[MI], bc[kNI];
@@ -415,34 +486,15 @@ __global__ void __launch_bounds__(kThreads) k_wgrad(WgradParams P) {
 #pragma unroll
         for (int ni = 0; ni < kNI; ++ni) acc[mi][ni] = floatx4{0, 0, 0, 0};
 
-    if (nstages > 0) {
-        load_slots(0);
-        dma(0);
-        load_slots(1);
-    }
-    for (int s = 0; s < nstages; ++s) {
-        wait_vmem_at_most<0>();
-        wait_lds_barrier();
-        if (s + 1 < nstages) {
-            dma(s + 1);
-            load_slots(s + 2);
-        }
-        const lds_u8* as = (const lds_u8*)smem + (s % kStages) * kStageBytes;
-        const lds_u8* bs = as + kColBytes;
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            bf16x8 af[MI], bf[kNI];
-#pragma unroll
-            for (int ni = 0; ni < kNI; ++ni) bf[ni] = frag_ro(bs, rd[ks] + bc[ni]);
-#pragma unroll
-            for (int mi = 0; mi < MI; ++mi) af[mi] = frag_ro(as, rd[ks] + ac[mi]);
-#pragma unroll
-            for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-                for (int ni = 0; ni < kNI; ++ni)
-                    acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[ni], af[mi], acc[mi][ni], 0, 0, 0);
-        }
-    }
+    load_slots(0);
+    if (nstages > 0)
+        run_stages<NS, MI, 2 * kDma, 2, 2>(
+            nstages, dma,
+            [&](int buf, int ks, int mi) { return frag_ro((const lds_u8*)smem + buf * kStageBytes, rd[ks] + ac[mi]); },
+            [&](int buf, int ks, int ni) {
+                return frag_ro((const lds_u8*)smem + buf * kStageBytes + kColBytes, rd[ks] + bc[ni]);
+            },
+            acc);
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
         const int n = n0 + wm * 128 + mi * 16 + lrow;
@@ -467,8 +519,8 @@ int64_t row_tiles_bound(int M, int E, int BM) { return M / BM + (int64_t)std::mi
 
 template <int FORM, int EPI, int BM>
 moe_status launch_rows(const MmParams& P, const char* name, hipStream_t s) {
-    const int64_t grid = (row_tiles_bound(P.M, P.E, BM) * P.ntc + 7) / 8 * 8;
-    const size_t lds = kStages * (BM * kBK * 2 + kColBytes);
+    const int64_t grid = xcd_grid(row_tiles_bound(P.M, P.E, BM) * P.ntc);
+    const size_t lds = stages<BM>() * (BM * kBK * 2 + kColBytes);
     moe_status st = allow_dynamic_lds(reinterpret_cast<const void*>(&k_rows_mm<FORM, EPI, BM>), lds);
     if (st != MOE_OK) return st;
     MOE_LAUNCH(name, (k_rows_mm<FORM, EPI, BM>), dim3((unsigned)grid), dim3(kThreads), lds, s, P);
@@ -545,8 +597,8 @@ moe_status launch_grouped_wgrad(const GroupedArgs& g, float* dw, bool accumulate
     P.ntk = (g.K + kBN - 1) / kBN;
     P.accumulate = accumulate;
     P.dw = dw;
-    const int64_t grid = ((int64_t)g.E * P.ntn * P.ntk + 7) / 8 * 8;
-    const size_t lds = kStages * 2 * kColBytes;
+    const int64_t grid = xcd_grid((int64_t)g.E * P.ntn * P.ntk);
+    const size_t lds = stages<kWM>() * 2 * kColBytes;
     moe_status st = allow_dynamic_lds(reinterpret_cast<const void*>(&k_wgrad), lds);
     if (st != MOE_OK) return st;
     MOE_LAUNCH("grouped_wgrad", k_wgrad, dim3((unsigned)grid), dim3(kThreads), lds, s, P);
