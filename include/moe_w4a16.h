@@ -414,7 +414,9 @@ moe_status moe_w4a16_shared_expert(const uint16_t *d_x, int32_t T, int32_t H, in
  * rows without weights.
  *
  * N and K multiples of 8 and at most 2^20; E <= 1024; X * K * 2 < 2^32 - 256
- * where rows are gathered (MOE_ERR_SHAPE).  Outputs overlap neither inputs nor
+ * where rows are gathered; fewer than 2^22 tiles: (M / 64 + E) * (max(N, K) /
+ * 128), for the weight gradient also E * (N / 128) * (K / 128)
+ * (MOE_ERR_SHAPE).  Outputs overlap neither inputs nor
  * each other (MOE_ERR_INVALID_ARG).  M == 0 is a no-op (moe_grouped_linear_wgrad
  * still writes dW).  Deterministic; nothing is allocated; graph-capturable.
  * There is no upper limit on d_offsets[E] - d_offsets[0] but M, and the host

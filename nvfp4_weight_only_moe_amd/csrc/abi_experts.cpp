@@ -158,7 +158,7 @@ moe_status moe_grouped_swiglu_dgrad(const uint16_t* d_dy, const uint16_t* d_w, i
 }
 
 size_t moe_grouped_linear_wgrad_workspace_size(int32_t M, int32_t N, int32_t K, int32_t E) {
-    if (check_group_shape(M, N, K, E) != MOE_OK || M == 0) return 0;
+    if (check_group_shape(M, N, K, E) != MOE_OK || !wgrad_grid_fits(N, K, E) || M == 0) return 0;
     return grouped_wgrad_workspace_bytes(M, N, K, E);
 }
 
@@ -168,6 +168,7 @@ moe_status moe_grouped_linear_wgrad(const uint16_t* d_dy, int32_t M, int32_t N, 
                                     hipStream_t stream) {
     moe_status st = check_group_shape(M, N, K, E);
     if (st != MOE_OK) return st;
+    if (!wgrad_grid_fits(N, K, E)) return MOE_ERR_SHAPE;
     if (accumulate != 0 && accumulate != 1) return MOE_ERR_INVALID_ARG;
     const Buf dw{d_dw, (size_t)E * N * K * 4}, off{d_offsets, (size_t)(E + 1) * 4};
     if ((st = check_present({off, dw})) != MOE_OK) return st;

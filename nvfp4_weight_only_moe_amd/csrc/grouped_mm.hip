@@ -23,7 +23,7 @@
 #include "device_common.h"
 #include "internal.h"
 
-#include <type_traits>
+#include <algorithm>
 
 namespace moe {
 namespace {
@@ -33,9 +33,6 @@ constexpr int kWaves = kThreads / kWave;
 constexpr int kBN = 256;                  // output columns per tile, 64 per wave
 constexpr int kNI = 4;                    // 16-column subtiles per wave
 constexpr int kBK = 64;                   // reduction steps per stage
-// LDS buffers of a stage (64 KB with 256 rows, 48 with 128, 40 with 64): what
-// fits 160 KB for one workgroup, with 64 rows for two.
-template <int BM> constexpr int stages() { return BM == 128 ? 3 : 2; }
 constexpr uint32_t kOutside = 0xFFFFFFFFu;
 constexpr uint32_t kRecords = 0xFFFFFF00u;   // descriptor size: every real offset is below it
 constexpr int kColBytes = kBN * kBK * 2;
@@ -81,57 +78,63 @@ __device__ __forceinline__ int slot_token(int slot, int k, uint32_t magic) {
 // then every wave has read all of the stage, its buffer takes the stage NS
 // later, and the next stage's first half is read under the second half's
 // MFMAs.  OPS: DMAs of a wave per stage, which complete in order.
-template <int NS, int U, int OPS, int READS_A, int READS_B, class Dma, class ReadA, class ReadB, class Acc>
+template <int OPS>
+__device__ __forceinline__ void wait_stages_behind(int n) {
+    if (n <= 0) wait_vmem_at_most<0>();
+    else if (n == 1) wait_vmem_at_most<OPS>();
+    else if (n == 2) wait_vmem_at_most<2 * OPS>();
+    else wait_vmem_at_most<3 * OPS>();
+}
+
+template <int NS, int U, int NI, int OPS, int READS_A, int READS_B, class Dma, class ReadA, class ReadB, class Acc>
 __device__ __forceinline__ void run_stages(int nstages, Dma&& dma, ReadA&& ra, ReadB&& rb, Acc& acc) {
 #pragma unroll
     for (int i = 0; i < NS; ++i)
         if (i < nstages) dma(i);
-    if (NS >= 3 && nstages >= 3) wait_vmem_at_most<2 * OPS>();
-    else if (nstages >= 2) wait_vmem_at_most<OPS>();
-    else wait_vmem_at_most<0>();
+    wait_stages_behind<OPS>(min(NS, nstages) - 1);
     wait_lds_barrier();
-    bf16x8 af[U], b0[kNI], b1[kNI];
+    bf16x8 af[U], b0[NI], b1[NI];
 #pragma unroll
-    for (int ni = 0; ni < kNI; ++ni) b0[ni] = rb(0, 0, ni);
+    for (int ni = 0; ni < NI; ++ni) b0[ni] = rb(0, 0, ni);
 #pragma unroll
     for (int mi = 0; mi < U; ++mi) af[mi] = ra(0, 0, mi);
     int buf = 0;
     for (int s = 0; s < nstages; ++s) {
 #pragma unroll
-        for (int ni = 0; ni < kNI; ++ni) b1[ni] = rb(buf, 1, ni);
+        for (int ni = 0; ni < NI; ++ni) b1[ni] = rb(buf, 1, ni);
 #pragma unroll
         for (int mi = 0; mi < U; ++mi) {
 #pragma unroll
-            for (int ni = 0; ni < kNI; ++ni)
+            for (int ni = 0; ni < NI; ++ni)
                 acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b0[ni], af[mi], acc[mi][ni], 0, 0, 0);
             af[mi] = ra(buf, 1, mi);
         }
-        __builtin_amdgcn_sched_group_barrier(0x100, kNI * READS_B, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, NI * READS_B, 0);
 #pragma unroll
         for (int mi = 0; mi < U; ++mi) {
-            __builtin_amdgcn_sched_group_barrier(0x008, kNI, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, NI, 0);
             __builtin_amdgcn_sched_group_barrier(0x100, READS_A, 0);
         }
         // stage s + 1 is in LDS (stages behind it may be in flight) and nobody reads stage s any more
-        if (NS >= 3 && s + 2 < nstages) wait_vmem_at_most<OPS>();
-        else wait_vmem_at_most<0>();
+        if constexpr (NS == 2) wait_vmem_at_most<0>();
+        else wait_stages_behind<OPS>(min(NS - 2, nstages - 2 - s));
         wait_lds_barrier();
         if (s + NS < nstages) dma(s + NS);
         buf = buf + 1 == NS ? 0 : buf + 1;
         // behind the last stage this reads a buffer whose values nobody uses
 #pragma unroll
-        for (int ni = 0; ni < kNI; ++ni) b0[ni] = rb(buf, 0, ni);
+        for (int ni = 0; ni < NI; ++ni) b0[ni] = rb(buf, 0, ni);
 #pragma unroll
         for (int mi = 0; mi < U; ++mi) {
 #pragma unroll
-            for (int ni = 0; ni < kNI; ++ni)
+            for (int ni = 0; ni < NI; ++ni)
                 acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1[ni], af[mi], acc[mi][ni], 0, 0, 0);
             af[mi] = ra(buf, 0, mi);
         }
-        __builtin_amdgcn_sched_group_barrier(0x100, kNI * READS_B, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, NI * READS_B, 0);
 #pragma unroll
         for (int mi = 0; mi < U; ++mi) {
-            __builtin_amdgcn_sched_group_barrier(0x008, kNI, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, NI, 0);
             __builtin_amdgcn_sched_group_barrier(0x100, READS_A, 0);
         }
     }
@@ -153,10 +156,6 @@ struct MmParams {
     int ntc;                      // column tiles
 };
 
-struct RowTile {
-    int e, p0, rows, ct;          // expert (-1: none), first row, rows of the tile, column tile
-};
-
 constexpr int kMGroup = 8;        // row tiles that run beside each other, sharing weight columns in L2
 
 // Number of workgroup `bid` among `total` tiles, or -1: the eight XCDs (which
@@ -171,51 +170,75 @@ __device__ __forceinline__ int xcd_tile(int bid, int total) {
 // workgroups that number at most `total` tiles that way
 int64_t xcd_grid(int64_t total) { return total + 8 * ((total + 255) / 256) + 8; }
 
-// Tile of workgroup `bid`: the tiles are numbered expert by expert.  Offsets
-// are clamped to [0, M], so no tile leaves the buffers.
+// The expert that holds tile number `t` of the launch, when every expert with
+// n rows has ceil(n / H) pieces (one, if n is 0 and EMPTY) of `per_piece`
+// tiles: its rows, the tile's number inside the expert, and how many pieces
+// the experts before it have that are cut in two or more.  Offsets are clamped to
+// [0, M], so no piece leaves the buffers.
+struct Piece {
+    int e, lo, n, pieces, idx, cut_before;
+};
+template <bool EMPTY>
+__device__ __forceinline__ Piece find_piece(const int32_t* __restrict__ offsets, int E, int M, int H, int per_piece,
+                                            int bid) {
+    const int lane = threadIdx.x & 63;
+    const int per = (E + kWave - 1) / kWave, b = lane * per;
+    const auto rows = [&](int e, int& lo) {
+        lo = max(offsets[e], 0);
+        return max(min(offsets[e + 1], M) - lo, 0);
+    };
+    const auto pieces = [&](int n) { return EMPTY ? max((n + H - 1) / H, 1) : (n + H - 1) / H; };
+    int local = 0, cut = 0, lo;
+    for (int i = 0; i < per; ++i)
+        if (b + i < E) {
+            const int k = pieces(rows(b + i, lo));
+            local += k;
+            cut += k > 1 ? k : 0;
+        }
+    const int incl = wave_inclusive_scan_dpp(local), cincl = wave_inclusive_scan_dpp(cut);
+    const int total = __builtin_amdgcn_readlane(incl, 63) * per_piece;
+    const int t = xcd_tile(bid, total);
+    if (t < 0) return Piece{-1, 0, 0, 0, 0, 0};
+    const int src = __ffsll((unsigned long long)__ballot(incl * per_piece > t)) - 1;
+    int first = __builtin_amdgcn_readlane(incl - local, src) * per_piece;
+    int before = __builtin_amdgcn_readlane(cincl - cut, src);
+    for (int i = 0; i < per; ++i) {
+        const int e = src * per + i, n = rows(e, lo), k = pieces(n);
+        if (t < first + k * per_piece)
+            return Piece{__builtin_amdgcn_readfirstlane(e), __builtin_amdgcn_readfirstlane(lo),
+                         __builtin_amdgcn_readfirstlane(n), __builtin_amdgcn_readfirstlane(k),
+                         __builtin_amdgcn_readfirstlane(t - first), __builtin_amdgcn_readfirstlane(before)};
+        first += k * per_piece;
+        before += k > 1 ? k : 0;
+    }
+    return Piece{-1, 0, 0, 0, 0, 0};
+}
+
+struct RowTile {
+    int e, p0, rows, ct;          // expert (-1: none), first row, rows of the tile, column tile
+};
+
+// Tile of workgroup `bid`: inside an expert, kMGroup row tiles by all column
+// tiles after each other.
 template <int BM>
 __device__ __forceinline__ RowTile find_tile(const MmParams& P, int bid) {
-    const int lane = threadIdx.x & 63;
-    const int per = (P.E + kWave - 1) / kWave, b = lane * per;
-    int local = 0;
-    for (int i = 0; i < per; ++i)
-        if (b + i < P.E) {
-            const int lo = max(P.offsets[b + i], 0), hi = min(P.offsets[b + i + 1], P.M);
-            local += (max(hi - lo, 0) + BM - 1) / BM * P.ntc;
-        }
-    const int incl = wave_inclusive_scan_dpp(local);
-    const int total = __builtin_amdgcn_readlane(incl, 63);
-    const int t = xcd_tile(bid, total);
-    RowTile d{-1, 0, 0, 0};
-    if (t < 0) return d;
-    const int src = __ffsll((unsigned long long)__ballot(incl > t)) - 1;
-    int first = __builtin_amdgcn_readlane(incl - local, src);
-    for (int i = 0; i < per; ++i) {
-        const int e = src * per + i;
-        const int lo = max(P.offsets[e], 0), hi = min(P.offsets[e + 1], P.M);
-        const int n = max(hi - lo, 0), mt = (n + BM - 1) / BM, tiles = mt * P.ntc;
-        if (t >= first + tiles) {
-            first += tiles;
-            continue;
-        }
-        const int L = t - first, full = mt / kMGroup * kMGroup;
-        int m, c;
-        if (L < full * P.ntc) {
-            const int g = L / (kMGroup * P.ntc), r = L % (kMGroup * P.ntc);
-            c = r / kMGroup;
-            m = g * kMGroup + r % kMGroup;
-        } else {
-            const int r = L - full * P.ntc, last = mt - full;
-            c = r / last;
-            m = full + r % last;
-        }
-        d.e = __builtin_amdgcn_readfirstlane(e);
-        d.p0 = __builtin_amdgcn_readfirstlane(lo + m * BM);
-        d.rows = __builtin_amdgcn_readfirstlane(min(BM, n - m * BM));
-        d.ct = __builtin_amdgcn_readfirstlane(c);
-        return d;
+    const Piece f = find_piece<false>(P.offsets, P.E, P.M, BM, P.ntc, bid);
+    if (f.e < 0) return RowTile{-1, 0, 0, 0};
+    const int full = f.pieces / kMGroup * kMGroup;
+    int m, c;
+    if (f.idx < full * P.ntc) {
+        const int g = f.idx / (kMGroup * P.ntc), r = f.idx % (kMGroup * P.ntc);
+        c = r / kMGroup;
+        m = g * kMGroup + r % kMGroup;
+    } else {
+        const int r = f.idx - full * P.ntc, last = f.pieces - full;
+        c = r / last;
+        m = full + r % last;
     }
-    return d;
+    // equal heights, whole subtiles: tiles that share weight columns then move
+    // through them in step and find each other's stages in L2
+    const int h = ((f.n + f.pieces - 1) / f.pieces + 15) & ~15;
+    return RowTile{f.e, f.lo + m * h, min(h, f.n - m * h), c};
 }
 
 // ---- fragments: lane l holds output position l & 15, reduction steps
@@ -223,9 +246,10 @@ __device__ __forceinline__ RowTile find_tile(const MmParams& P, int bid) {
 __device__ __forceinline__ bf16x8 frag_rc(const lds_u8* tile, int lane_off, int sub) {
     return *reinterpret_cast<const __attribute__((address_space(3))) bf16x8*>(tile + lane_off + sub * 2048);
 }
+template <int ROW>                          // bytes of an LDS row
 __device__ __forceinline__ bf16x8 frag_ro(const lds_u8* tile, int lane_off) {
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + lane_off));
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + lane_off + 4 * 512));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + lane_off + 4 * ROW));
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 __device__ __forceinline__ int ro_swizzle(int row) { return (row & 3) | ((row >> 1) & 4); }
@@ -242,19 +266,17 @@ __device__ __forceinline__ floatx4 load4(const uint16_t* p) {
                    bf16_bits_to_f32(u.y >> 16)};
 }
 
-template <int FORM, int EPI, int BM>
-__global__ void __launch_bounds__(kThreads, BM == 64 ? 4 : 2) k_rows_mm(MmParams P) {
-    constexpr int MI = BM / 32;                     // 16-row subtiles per wave
-    constexpr int NS = stages<BM>();
+constexpr int rows_lds(int BM, int NS) { return NS * (BM * kBK * 2 + kColBytes); }
+
+// One tile: U of each wave's BM / 32 16-row subtiles.  The two waves of a SIMD
+// take the tile's subtiles in turn, so a short tile costs both the same.
+template <int FORM, int EPI, int BM, int U, int NS>
+__device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, uint8_t* smem) {
     constexpr int kRowBytes = BM * kBK * 2;
     constexpr int kStageBytes = kRowBytes + kColBytes;
     constexpr int kADma = kRowBytes / 1024 / kWaves, kBDma = kColBytes / 1024 / kWaves;
     constexpr bool kGateUp = FORM == kNT && EPI == kSwiglu;   // 128 gate + 128 up columns per tile
     constexpr int kTileCols = kGateUp ? kBN / 2 : kBN;        // output columns per tile
-    extern __shared__ __align__(16) uint8_t smem[];
-
-    const RowTile t = find_tile<BM>(P, blockIdx.x);
-    if (t.e < 0) return;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave >> 2, wn = wave & 3;
@@ -334,38 +356,24 @@ __global__ void __launch_bounds__(kThreads, BM == 64 ? 4 : 2) k_rows_mm(MmParams
 #pragma unroll
     for (int ni = 0; ni < kNI; ++ni) bchunk[ni] = ((wn * 4 + ni) ^ bsw) * 32;
 
-    floatx4 acc[MI][kNI];
+    floatx4 acc[U][kNI];
 #pragma unroll
-    for (int mi = 0; mi < MI; ++mi)
+    for (int mi = 0; mi < U; ++mi)
 #pragma unroll
         for (int ni = 0; ni < kNI; ++ni) acc[mi][ni] = floatx4{0, 0, 0, 0};
-
-    // the stages, for the first U of each wave's 16-row subtiles
-    const auto run = [&](auto used) {
-        constexpr int U = decltype(used)::value;
-        run_stages<NS, U, kADma + kBDma, 1, FORM == kNT ? 1 : 2>(
-            nstages, dma,
-            [&](int buf, int ks, int mi) { return frag_rc((const lds_u8*)smem + buf * kStageBytes, aread[ks], 2 * mi); },
-            [&](int buf, int ks, int ni) {
-                const lds_u8* bs = (const lds_u8*)smem + buf * kStageBytes + kRowBytes;
-                if constexpr (FORM == kNT) return frag_rc(bs, bread[ks], kGateUp && ni >= 2 ? ni + 6 : ni);
-                else return frag_ro(bs, bread[ks] + bchunk[ni]);
-            },
-            acc);
-    };
-    // The two waves of a SIMD take the tile's 16-row subtiles in turn, so a
-    // short tile costs both the same; five copies of the loop (1, 2, 4, 6 or 8
-    // subtiles a wave) leave out what lies behind the tile's last row.
-    const int need = (t.rows + 31) >> 5;
-    if (need <= 1) run(std::integral_constant<int, 1>{});
-    else if (MI <= 2 || need <= 2) run(std::integral_constant<int, 2>{});
-    else if (MI <= 4 || need <= 4) run(std::integral_constant<int, (MI < 4 ? MI : 4)>{});
-    else if (need <= 6) run(std::integral_constant<int, (MI < 6 ? MI : 6)>{});
-    else run(std::integral_constant<int, MI>{});
+    run_stages<NS, U, kNI, kADma + kBDma, 1, FORM == kNT ? 1 : 2>(
+        nstages, dma,
+        [&](int buf, int ks, int mi) { return frag_rc((const lds_u8*)smem + buf * kStageBytes, aread[ks], 2 * mi); },
+        [&](int buf, int ks, int ni) {
+            const lds_u8* bs = (const lds_u8*)smem + buf * kStageBytes + kRowBytes;
+            if constexpr (FORM == kNT) return frag_rc(bs, bread[ks], kGateUp && ni >= 2 ? ni + 6 : ni);
+            else return frag_ro<512>(bs, bread[ks] + bchunk[ni]);
+        },
+        acc);
 
     // one rounding to bf16 per output
 #pragma unroll
-    for (int mi = 0; mi < MI; ++mi) {
+    for (int mi = 0; mi < U; ++mi) {
         const int r = mi * 32 + wm * 16 + lrow;
         if (r >= t.rows) continue;
         const int64_t row = (int64_t)(t.p0 + r) * P.C;
@@ -402,6 +410,26 @@ __global__ void __launch_bounds__(kThreads, BM == 64 ? 4 : 2) k_rows_mm(MmParams
     }
 }
 
+// Tiles of up to BM rows, by their rows: a short tile waits for memory, not
+// for the matrix units, and its smaller stages leave room for more of them in
+// flight (2 to 4 of 64 to 40 KB in 160 KB of LDS).  BM == 64: two workgroups a CU instead.
+template <int FORM, int EPI, int BM>
+__global__ void __launch_bounds__(kThreads, BM == 64 ? 4 : 2) k_rows_mm(MmParams P) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    constexpr int NS64 = BM == 64 ? 2 : 4;
+    const RowTile t = find_tile<BM>(P, blockIdx.x);
+    if (t.e < 0) return;
+    if (t.rows <= 32) rows_tile<FORM, EPI, 64, 1, NS64>(P, t, smem);
+    else if (BM == 64 || t.rows <= 64) rows_tile<FORM, EPI, 64, 2, NS64>(P, t, smem);
+    else if constexpr (BM > 64) {
+        if (t.rows <= 96) rows_tile<FORM, EPI, 128, 3, 3>(P, t, smem);
+        else if (t.rows <= 128) rows_tile<FORM, EPI, 128, 4, 3>(P, t, smem);
+        else if (t.rows <= 160) rows_tile<FORM, EPI, 192, 5, 2>(P, t, smem);
+        else if (t.rows <= 192) rows_tile<FORM, EPI, 192, 6, 2>(P, t, smem);
+        else rows_tile<FORM, EPI, 256, 8, 2>(P, t, smem);
+    }
+}
+
 // ---------------------------------------------------------------- weight gradient
 struct WgradParams {
     const uint16_t* dy;           // [M][N]
@@ -411,35 +439,47 @@ struct WgradParams {
     int E, M, X, k;
     uint32_t kmagic;
     int N, K, ntn, ntk;
+    int slice;                    // rows of a slice of the reduction
     int accumulate;
     float* dw;                    // [E][N][K]
+    float* part;                  // fp32 [N][K] per slice of the experts that have two or more
+    int parts;                    // how many fit (offsets that are not ascending could ask for more)
 };
 
-constexpr int kWM = 256;          // rows n of a wgrad tile
-
-__global__ void __launch_bounds__(kThreads) k_wgrad(WgradParams P) {
-    constexpr int MI = kWM / 32, kDma = 4, NS = stages<kWM>();
-    constexpr int kStageBytes = 2 * kColBytes;
+// One workgroup: a tile of 32 MI x 64 NI of one expert's dW over one slice of its rows.
+template <int MI, int NI, int NS>
+__global__ void __launch_bounds__(kThreads, MI * NI <= 8 ? 4 : 2) k_wgrad(WgradParams P) {
+    constexpr int TM = MI * 32, TN = NI * 64;                       // rows n, columns k of the tile
+    constexpr int kABytes = TM * kBK * 2, kBBytes = TN * kBK * 2, kStageBytes = kABytes + kBBytes;
+    constexpr int kADma = kABytes / 1024 / kWaves, kBDma = kBBytes / 1024 / kWaves;
+    constexpr int kARows = 512 / TM, kBRows = 512 / TN;             // LDS rows per DMA
     extern __shared__ __align__(16) uint8_t smem[];
-    const int per_e = P.ntn * P.ntk;
-    const int tile = xcd_tile(blockIdx.x, P.E * per_e);
-    if (tile < 0) return;
-    const int e = tile / per_e, n0 = tile % per_e % P.ntn * kWM, k0 = tile % per_e / P.ntn * kBN;
-    const int p0 = max(P.offsets[e], 0), cnt = max(min(P.offsets[e + 1], P.M) - p0, 0);
+    const int per = P.ntn * P.ntk;
+    const Piece f = find_piece<true>(P.offsets, P.E, P.M, P.slice, per, blockIdx.x);
+    if (f.e < 0) return;
+    const int e = f.e, sl = f.idx / per, tile = f.idx % per;
+    const int n0 = tile % P.ntn * TM, k0 = tile / P.ntn * TN;
+    const int p0 = f.lo + sl * P.slice, cnt = min(f.n - sl * P.slice, P.slice);
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave >> 2, wn = wave & 3;
     const int lrow = lane & 15, q = lane >> 4;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_u8*)smem;
 
-    uint32_t aoff[kDma], xcol[kDma];
-    int rr[kDma], slot[kDma];
+    // a lane's LDS row and the columns that it fetches, per DMA
+    uint32_t aoff[kADma], xcol[kBDma];
+    int arow[kADma], xrow[kBDma], slot[kBDma];
+    const auto column = [&](int r, int pos) { return (((pos >> 1) ^ ro_swizzle(r)) << 4) + ((pos & 1) << 3); };
 #pragma unroll
-    for (int i = 0; i < kDma; ++i) {
-        const int r = (i * kWaves + wave) * 2 + (lane >> 5);
-        const int pos = lane & 31, col = (((pos >> 1) ^ ro_swizzle(r)) << 4) + ((pos & 1) << 3);
-        rr[i] = r;
+    for (int i = 0; i < kADma; ++i) {
+        const int r = (i * kWaves + wave) * kARows + lane / (64 / kARows), col = column(r, lane % (64 / kARows));
+        arow[i] = r;
         aoff[i] = n0 + col < P.N ? (uint32_t)r * (uint32_t)P.N * 2u + col * 2 : kOutside;
+    }
+#pragma unroll
+    for (int i = 0; i < kBDma; ++i) {
+        const int r = (i * kWaves + wave) * kBRows + lane / (64 / kBRows), col = column(r, lane % (64 / kBRows));
+        xrow[i] = r;
         xcol[i] = k0 + col < P.K ? (uint32_t)col * 2u : kOutside;
         slot[i] = 0;
     }
@@ -447,7 +487,7 @@ __global__ void __launch_bounds__(kThreads) k_wgrad(WgradParams P) {
     const auto load_slots = [&](int s) {
         if (!P.slots) return;
 #pragma unroll
-        for (int i = 0; i < kDma; ++i) slot[i] = P.slots[min(p0 + s * kBK + rr[i], P.M - 1)];
+        for (int i = 0; i < kBDma; ++i) slot[i] = P.slots[min(p0 + s * kBK + xrow[i], P.M - 1)];
     };
     const auto dma = [&](int s) {
         const int r0 = s * kBK;
@@ -455,60 +495,99 @@ __global__ void __launch_bounds__(kThreads) k_wgrad(WgradParams P) {
         const uint16_t* a = uniform_ptr(P.dy + (int64_t)(p0 + r0) * P.N + n0);
         const uint16_t* x = uniform_ptr(P.x + (P.slots ? 0 : (int64_t)(p0 + r0) * P.K) + k0);
 #pragma unroll
-        for (int i = 0; i < kDma; ++i)
-            lds_dma16_buf(a, r0 + rr[i] < cnt ? aoff[i] : kOutside, buf + (i * kWaves + wave) * 1024);
+        for (int i = 0; i < kADma; ++i)
+            lds_dma16_buf(a, r0 + arow[i] < cnt ? aoff[i] : kOutside, buf + (i * kWaves + wave) * 1024);
 #pragma unroll
-        for (int i = 0; i < kDma; ++i) {
-            int src = rr[i];
-            bool ok = r0 + rr[i] < cnt && xcol[i] != kOutside;
+        for (int i = 0; i < kBDma; ++i) {
+            int src = xrow[i];
+            bool ok = r0 + xrow[i] < cnt && xcol[i] != kOutside;
             if (P.slots) {
                 src = slot_token(slot[i], P.k, P.kmagic);
                 ok = ok && slot[i] >= 0 && src < P.X;
             }
             lds_dma16_buf(x, ok ? (uint32_t)src * (uint32_t)P.K * 2u + xcol[i] : kOutside,
-                          buf + kColBytes + (i * kWaves + wave) * 1024);
+                          buf + kABytes + (i * kWaves + wave) * 1024);
         }
         load_slots(s + 1);                          // for the next call
     };
 
-    int rd[2], ac[MI], bc[kNI];
+    int ard[2], brd[2], ac[MI], bc[NI];
     const int sw = (lrow >> 2) | ((q & 1) << 2);
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) rd[ks] = (ks * 32 + q * 8 + (lrow >> 2)) * 512 + (lrow & 3) * 8;
+    for (int ks = 0; ks < 2; ++ks) {
+        const int r = ks * 32 + q * 8 + (lrow >> 2);
+        ard[ks] = r * TM * 2 + (lrow & 3) * 8;
+        brd[ks] = r * TN * 2 + (lrow & 3) * 8;
+    }
 #pragma unroll
-    for (int mi = 0; mi < MI; ++mi) ac[mi] = ((wm * 8 + mi) ^ sw) * 32;
+    for (int mi = 0; mi < MI; ++mi) ac[mi] = ((wm * MI + mi) ^ sw) * 32;
 #pragma unroll
-    for (int ni = 0; ni < kNI; ++ni) bc[ni] = ((wn * 4 + ni) ^ sw) * 32;
+    for (int ni = 0; ni < NI; ++ni) bc[ni] = ((wn * NI + ni) ^ sw) * 32;
 
-    floatx4 acc[MI][kNI];
+    floatx4 acc[MI][NI];
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
-        for (int ni = 0; ni < kNI; ++ni) acc[mi][ni] = floatx4{0, 0, 0, 0};
+        for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = floatx4{0, 0, 0, 0};
 
     load_slots(0);
     if (nstages > 0)
-        run_stages<NS, MI, 2 * kDma, 2, 2>(
+        run_stages<NS, MI, NI, kADma + kBDma, 2, 2>(
             nstages, dma,
-            [&](int buf, int ks, int mi) { return frag_ro((const lds_u8*)smem + buf * kStageBytes, rd[ks] + ac[mi]); },
+            [&](int buf, int ks, int mi) {
+                return frag_ro<TM * 2>((const lds_u8*)smem + buf * kStageBytes, ard[ks] + ac[mi]);
+            },
             [&](int buf, int ks, int ni) {
-                return frag_ro((const lds_u8*)smem + buf * kStageBytes + kColBytes, rd[ks] + bc[ni]);
+                return frag_ro<TN * 2>((const lds_u8*)smem + buf * kStageBytes + kABytes, brd[ks] + bc[ni]);
             },
             acc);
+    const bool whole = f.pieces == 1;
+    if (!whole && f.cut_before + sl >= P.parts) return;
+    float* base = whole ? P.dw + (int64_t)e * P.N * P.K : P.part + (int64_t)(f.cut_before + sl) * P.N * P.K;
+    const bool add = whole && P.accumulate;
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
-        const int n = n0 + wm * 128 + mi * 16 + lrow;
+        const int n = n0 + (wm * MI + mi) * 16 + lrow;
         if (n >= P.N) continue;
-        float* row = P.dw + ((int64_t)e * P.N + n) * P.K;
+        float* row = base + (int64_t)n * P.K;
 #pragma unroll
-        for (int ni = 0; ni < kNI; ++ni) {
-            const int c = k0 + wn * 64 + ni * 16 + q * 4;
+        for (int ni = 0; ni < NI; ++ni) {
+            const int c = k0 + (wn * NI + ni) * 16 + q * 4;
             if (c >= P.K) continue;
             floatx4 v = acc[mi][ni];
-            if (P.accumulate) v += *reinterpret_cast<const floatx4*>(row + c);
+            if (add) v += *reinterpret_cast<const floatx4*>(row + c);
             *reinterpret_cast<floatx4*>(row + c) = v;
         }
     }
+}
+
+// dW of the experts whose rows were cut into slices: the slices' sums, in order.
+__global__ void __launch_bounds__(256) k_wgrad_join(WgradParams P) {
+    const int lane = threadIdx.x & 63, e = blockIdx.y;
+    int before = 0, pieces = 0;
+    for (int b = 0; b <= e; b += kWave) {
+        int k = 0;
+        if (b + lane <= e) {
+            const int lo = max(P.offsets[b + lane], 0), n = min(P.offsets[b + lane + 1], P.M) - lo;
+            k = (max(n, 0) + P.slice - 1) / P.slice;
+            if (k <= 1) k = 0;
+        }
+        if (b + kWave > e) {
+            pieces = __builtin_amdgcn_readlane(k, e - b);
+            if (lane >= e - b) k = 0;
+        }
+        before += __builtin_amdgcn_readlane(wave_inclusive_scan_dpp(k), 63);
+    }
+    pieces = min(pieces, P.parts - before);
+    if (pieces <= 1) return;
+    const int64_t size = (int64_t)P.N * P.K, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= size) return;
+    const float* part = P.part + before * size + i;
+    float* dw = P.dw + e * size + i;
+    floatx4 v = {0, 0, 0, 0};
+    if (P.accumulate) v = *reinterpret_cast<const floatx4*>(dw);
+    for (int s = 0; s < pieces; ++s) v += *reinterpret_cast<const floatx4*>(part + s * size);
+    *reinterpret_cast<floatx4*>(dw) = v;
 }
 
 uint32_t div_magic(int k) { return k <= 1 ? 0u : (uint32_t)((1ull << 32) / (uint32_t)k); }
@@ -520,7 +599,7 @@ int64_t row_tiles_bound(int M, int E, int BM) { return M / BM + (int64_t)std::mi
 template <int FORM, int EPI, int BM>
 moe_status launch_rows(const MmParams& P, const char* name, hipStream_t s) {
     const int64_t grid = xcd_grid(row_tiles_bound(P.M, P.E, BM) * P.ntc);
-    const size_t lds = stages<BM>() * (BM * kBK * 2 + kColBytes);
+    const size_t lds = BM == 64 ? rows_lds(64, 2) : std::max({rows_lds(64, 4), rows_lds(128, 3), rows_lds(256, 2)});
     moe_status st = allow_dynamic_lds(reinterpret_cast<const void*>(&k_rows_mm<FORM, EPI, BM>), lds);
     if (st != MOE_OK) return st;
     MOE_LAUNCH(name, (k_rows_mm<FORM, EPI, BM>), dim3((unsigned)grid), dim3(kThreads), lds, s, P);
@@ -530,9 +609,44 @@ moe_status launch_rows(const MmParams& P, const char* name, hipStream_t s) {
 template <int FORM, int EPI>
 moe_status launch_rows_any(const MmParams& P, const char* name, hipStream_t s) {
     const int64_t mean = P.M / std::max(1, std::min(P.E, P.M));
-    if (mean > 128) return launch_rows<FORM, EPI, 256>(P, name, s);
-    if (mean > 48) return launch_rows<FORM, EPI, 128>(P, name, s);
+    if (mean > 48) return launch_rows<FORM, EPI, 256>(P, name, s);
     return launch_rows<FORM, EPI, 64>(P, name, s);
+}
+
+// Tile of a weight gradient and rows of a slice of its reduction.
+struct WgradPlan {
+    bool big;
+    int ntn, ntk, slice, parts;
+    int64_t tiles, part_bytes;
+};
+
+WgradPlan wgrad_plan(int M, int N, int K, int E) {
+    WgradPlan p{};
+    const int64_t big_tiles = (int64_t)((N + 255) / 256) * ((K + 255) / 256) * E;
+    p.big = big_tiles >= 256;
+    const int T = p.big ? 256 : 128;
+    p.ntn = (N + T - 1) / T;
+    p.ntk = (K + T - 1) / T;
+    const int64_t per = (int64_t)p.ntn * p.ntk, slots = p.big ? 256 : 512;
+    p.slice = 1 << 30;
+    if (per * E < slots) {
+        const int64_t want = std::max<int64_t>(1, slots / per), stages = (M + kBK - 1) / kBK;
+        const int64_t rows = std::max<int64_t>((stages + want - 1) / want, 4) * kBK;
+        if (rows < M) p.slice = (int)rows;
+    }
+    p.parts = p.slice < M ? 2 * (M / p.slice) + 2 : 0;
+    p.part_bytes = (int64_t)p.parts * N * K * 4;
+    p.tiles = (p.slice < M ? M / p.slice + (int64_t)E : E) * per;
+    return p;
+}
+
+template <int MI, int NI, int NS>
+moe_status launch_wgrad(const WgradParams& P, int64_t tiles, hipStream_t s) {
+    const size_t lds = NS * (MI * 32 + NI * 64) * kBK * 2;
+    moe_status st = allow_dynamic_lds(reinterpret_cast<const void*>(&k_wgrad<MI, NI, NS>), lds);
+    if (st != MOE_OK) return st;
+    MOE_LAUNCH("grouped_wgrad", (k_wgrad<MI, NI, NS>), dim3((unsigned)xcd_grid(tiles)), dim3(kThreads), lds, s, P);
+    return MOE_OK;
 }
 
 }  // namespace
@@ -540,6 +654,8 @@ moe_status launch_rows_any(const MmParams& P, const char* name, hipStream_t s) {
 bool grouped_grid_fits(int M, int E, int C) {
     return (M / 64 + (int64_t)std::min(E, M)) * ((C + 127) / 128) < (1 << 22);
 }
+
+bool wgrad_grid_fits(int N, int K, int E) { return (int64_t)E * ((N + 127) / 128) * ((K + 127) / 128) < (1 << 22); }
 
 moe_status launch_grouped_fwd(const GroupedArgs& g, hipStream_t s) {
     MmParams P{};
@@ -579,12 +695,11 @@ moe_status launch_grouped_dgrad(const GroupedArgs& g, hipStream_t s) {
 }
 
 size_t grouped_wgrad_workspace_bytes(int M, int N, int K, int E) {
-    (void)M; (void)N; (void)K; (void)E;
-    return 0;
+    return (size_t)wgrad_plan(M, N, K, E).part_bytes;
 }
 
 moe_status launch_grouped_wgrad(const GroupedArgs& g, float* dw, bool accumulate, void* ws, hipStream_t s) {
-    (void)ws;
+    const WgradPlan p = wgrad_plan(g.M, g.N, g.K, g.E);
     WgradParams P{};
     P.dy = g.dy;
     P.x = g.x;
@@ -593,15 +708,17 @@ moe_status launch_grouped_wgrad(const GroupedArgs& g, float* dw, bool accumulate
     P.E = g.E; P.M = g.M; P.X = g.X; P.k = g.k;
     P.kmagic = div_magic(g.k);
     P.N = g.N; P.K = g.K;
-    P.ntn = (g.N + kWM - 1) / kWM;
-    P.ntk = (g.K + kBN - 1) / kBN;
+    P.ntn = p.ntn;
+    P.ntk = p.ntk;
+    P.slice = p.slice;
     P.accumulate = accumulate;
     P.dw = dw;
-    const int64_t grid = xcd_grid((int64_t)g.E * P.ntn * P.ntk);
-    const size_t lds = stages<kWM>() * 2 * kColBytes;
-    moe_status st = allow_dynamic_lds(reinterpret_cast<const void*>(&k_wgrad), lds);
-    if (st != MOE_OK) return st;
-    MOE_LAUNCH("grouped_wgrad", k_wgrad, dim3((unsigned)grid), dim3(kThreads), lds, s, P);
+    P.part = static_cast<float*>(ws);
+    P.parts = p.parts;
+    const moe_status st = p.big ? launch_wgrad<8, 4, 2>(P, p.tiles, s) : launch_wgrad<4, 2, 2>(P, p.tiles, s);
+    if (st != MOE_OK || p.part_bytes == 0) return st;
+    MOE_LAUNCH("grouped_wgrad_join", k_wgrad_join, dim3((unsigned)(((int64_t)g.N * g.K + 1023) / 1024), g.E), dim3(256),
+               0, s, P);
     return MOE_OK;
 }
 

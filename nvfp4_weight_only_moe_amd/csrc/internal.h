@@ -141,6 +141,7 @@ struct GroupedArgs {
     uint16_t *o0, *o1, *o2;     // y | h, a, b | dx | da, db
 };
 bool grouped_grid_fits(int M, int E, int C);   // the launch of M rows and C output columns
+bool wgrad_grid_fits(int N, int K, int E);
 moe_status launch_grouped_fwd(const GroupedArgs& g, hipStream_t s);      // w2 set: gate/up with SwiGLU
 moe_status launch_grouped_dgrad(const GroupedArgs& g, hipStream_t s);    // a set: through SwiGLU
 size_t grouped_wgrad_workspace_bytes(int M, int N, int K, int E);
