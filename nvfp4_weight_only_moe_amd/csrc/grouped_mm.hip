@@ -72,12 +72,13 @@ __device__ __forceinline__ int slot_token(int slot, int k, uint32_t magic) {
     return (int)q;
 }
 
-// The stages of a tile, through a ring of NS LDS buffers.  Fragments are read
+// The stages of a tile, through rings of NSA and NSB LDS buffers for the two
+// operands.  Fragments are read
 // one k-step ahead: while the MFMAs of a stage's first half run, its second
 // half is read (in place, a fragment as soon as its four MFMAs are issued);
-// then every wave has read all of the stage, its buffer takes the stage NS
-// later, and the next stage's first half is read under the second half's
-// MFMAs.  OPS: DMAs of a wave per stage, which complete in order.
+// then every wave has read all of the stage, its buffers take the stages NSA
+// and NSB later, and the next stage's first half is read under the second half's
+// MFMAs.  OPSA, OPSB: DMAs of a wave per stage, which complete in order.
 template <int OPS>
 __device__ __forceinline__ void wait_stages_behind(int n) {
     if (n <= 0) wait_vmem_at_most<0>();
@@ -86,28 +87,35 @@ __device__ __forceinline__ void wait_stages_behind(int n) {
     else wait_vmem_at_most<3 * OPS>();
 }
 
-template <int NS, int U, int NI, int OPS, int READS_A, int READS_B, class Dma, class ReadA, class ReadB, class Acc>
-__device__ __forceinline__ void run_stages(int nstages, Dma&& dma, ReadA&& ra, ReadB&& rb, Acc& acc) {
+template <int NSA, int NSB, int U, int NI, int OPSA, int OPSB, int READS_A, int READS_B, class DmaA, class DmaB,
+          class ReadA, class ReadB, class Acc>
+__device__ __forceinline__ void run_stages(int nstages, DmaA&& dma_a, DmaB&& dma_b, ReadA&& ra, ReadB&& rb, Acc& acc) {
+    constexpr int OPS = OPSA + OPSB;
+    static_assert(NSB == NSA || (NSA == 2 && NSB == 3), "the waits below");
 #pragma unroll
-    for (int i = 0; i < NS; ++i)
-        if (i < nstages) dma(i);
-    wait_stages_behind<OPS>(min(NS, nstages) - 1);
+    for (int i = 0; i < NSB; ++i) {
+        if (i < NSA && i < nstages) dma_a(i);
+        if (i < nstages) dma_b(i);
+    }
+    if constexpr (NSA == NSB) wait_stages_behind<OPS>(min(NSA, nstages) - 1);
+    else if (nstages > 2) wait_vmem_at_most<OPS + OPSB>();
+    else wait_stages_behind<OPS>(nstages - 1);
     wait_lds_barrier();
     bf16x8 af[U], b0[NI], b1[NI];
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni) b0[ni] = rb(0, 0, ni);
 #pragma unroll
     for (int mi = 0; mi < U; ++mi) af[mi] = ra(0, 0, mi);
-    int buf = 0;
+    int bufa = 0, bufb = 0;
     for (int s = 0; s < nstages; ++s) {
 #pragma unroll
-        for (int ni = 0; ni < NI; ++ni) b1[ni] = rb(buf, 1, ni);
+        for (int ni = 0; ni < NI; ++ni) b1[ni] = rb(bufb, 1, ni);
 #pragma unroll
         for (int mi = 0; mi < U; ++mi) {
 #pragma unroll
             for (int ni = 0; ni < NI; ++ni)
                 acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b0[ni], af[mi], acc[mi][ni], 0, 0, 0);
-            af[mi] = ra(buf, 1, mi);
+            af[mi] = ra(bufa, 1, mi);
         }
         __builtin_amdgcn_sched_group_barrier(0x100, NI * READS_B, 0);
 #pragma unroll
@@ -116,20 +124,23 @@ __device__ __forceinline__ void run_stages(int nstages, Dma&& dma, ReadA&& ra, R
             __builtin_amdgcn_sched_group_barrier(0x100, READS_A, 0);
         }
         // stage s + 1 is in LDS (stages behind it may be in flight) and nobody reads stage s any more
-        if constexpr (NS == 2) wait_vmem_at_most<0>();
-        else wait_stages_behind<OPS>(min(NS - 2, nstages - 2 - s));
+        if constexpr (NSA != NSB) wait_stages_behind<OPSB>(min(1, nstages - 2 - s));
+        else if constexpr (NSA == 2) wait_vmem_at_most<0>();
+        else wait_stages_behind<OPS>(min(NSA - 2, nstages - 2 - s));
         wait_lds_barrier();
-        if (s + NS < nstages) dma(s + NS);
-        buf = buf + 1 == NS ? 0 : buf + 1;
+        if (s + NSA < nstages) dma_a(s + NSA);
+        if (s + NSB < nstages) dma_b(s + NSB);
+        bufa = bufa + 1 == NSA ? 0 : bufa + 1;
+        bufb = bufb + 1 == NSB ? 0 : bufb + 1;
         // behind the last stage this reads a buffer whose values nobody uses
 #pragma unroll
-        for (int ni = 0; ni < NI; ++ni) b0[ni] = rb(buf, 0, ni);
+        for (int ni = 0; ni < NI; ++ni) b0[ni] = rb(bufb, 0, ni);
 #pragma unroll
         for (int mi = 0; mi < U; ++mi) {
 #pragma unroll
             for (int ni = 0; ni < NI; ++ni)
                 acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1[ni], af[mi], acc[mi][ni], 0, 0, 0);
-            af[mi] = ra(buf, 0, mi);
+            af[mi] = ra(bufa, 0, mi);
         }
         __builtin_amdgcn_sched_group_barrier(0x100, NI * READS_B, 0);
 #pragma unroll
@@ -254,26 +265,45 @@ __device__ __forceinline__ bf16x8 frag_ro(const lds_u8* tile, int lane_off) {
 }
 __device__ __forceinline__ int ro_swizzle(int row) { return (row & 3) | ((row >> 1) & 4); }
 
+// Two floats to a bf16 pair, round to nearest even (v_cvt_pk_bf16_f32).
 __device__ __forceinline__ uint32_t pack_rne(float lo, float hi) {
-    return (uint32_t)f32_to_bf16_rne(lo) | ((uint32_t)f32_to_bf16_rne(hi) << 16);
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((floatx2){lo, hi}, bf16x2));
 }
-__device__ __forceinline__ void store4(uint16_t* p, floatx4 v) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_rne(v[0], v[1]), pack_rne(v[2], v[3]));
+// sigmoid with the reciprocal and exponential instructions (a few 2^-23 relative)
+__device__ __forceinline__ float sigmoid(float a) { return __builtin_amdgcn_rcpf(1.0f + __expf(-a)); }
+
+// A lane's four columns of two neighbouring 16-column subtiles <-> eight
+// columns of one of them: lane rows (16 lanes) 0 and 1 trade halves, and 2 and
+// 3.  Afterwards lane row q holds columns 8 (q >> 1) .. + 7 of subtile q & 1,
+// 16 bytes of bf16.  The exchange undoes itself.
+struct Pair4 {
+    uint32_t a0, a1, b0, b1;      // subtile a: columns 0, 1 | 2, 3; subtile b the same
+};
+__device__ __forceinline__ uint4 exchange(Pair4 v) {
+    const auto x = __builtin_amdgcn_permlane16_swap(v.a0, v.b0, false, false);
+    const auto y = __builtin_amdgcn_permlane16_swap(v.a1, v.b1, false, false);
+    return make_uint4(x[0], y[0], x[1], y[1]);
 }
-__device__ __forceinline__ floatx4 load4(const uint16_t* p) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    return floatx4{bf16_bits_to_f32(u.x & 0xFFFFu), bf16_bits_to_f32(u.x >> 16), bf16_bits_to_f32(u.y & 0xFFFFu),
-                   bf16_bits_to_f32(u.y >> 16)};
+__device__ __forceinline__ Pair4 exchange_back(uint4 v) {
+    const auto x = __builtin_amdgcn_permlane16_swap(v.x, v.z, false, false);
+    const auto y = __builtin_amdgcn_permlane16_swap(v.y, v.w, false, false);
+    return Pair4{x[0], y[0], x[1], y[1]};
+}
+__device__ __forceinline__ uint4 pack_pair(floatx4 a, floatx4 b) {
+    return exchange(Pair4{pack_rne(a[0], a[1]), pack_rne(a[2], a[3]), pack_rne(b[0], b[1]), pack_rne(b[2], b[3])});
+}
+__device__ __forceinline__ floatx4 widen4(uint32_t lo, uint32_t hi) {
+    return floatx4{bf16_bits_to_f32(lo & 0xFFFFu), __uint_as_float(lo & 0xFFFF0000u), bf16_bits_to_f32(hi & 0xFFFFu),
+                   __uint_as_float(hi & 0xFFFF0000u)};
 }
 
-constexpr int rows_lds(int BM, int NS) { return NS * (BM * kBK * 2 + kColBytes); }
+constexpr int rows_lds(int BM, int NSA, int NSB) { return NSA * BM * kBK * 2 + NSB * kColBytes; }
 
 // One tile: U of each wave's BM / 32 16-row subtiles.  The two waves of a SIMD
 // take the tile's subtiles in turn, so a short tile costs both the same.
-template <int FORM, int EPI, int BM, int U, int NS>
+template <int FORM, int EPI, int BM, int U, int NSA, int NSB>
 __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, uint8_t* smem) {
-    constexpr int kRowBytes = BM * kBK * 2;
-    constexpr int kStageBytes = kRowBytes + kColBytes;
+    constexpr int kRowBytes = BM * kBK * 2, kColRing = NSA * kRowBytes;
     constexpr int kADma = kRowBytes / 1024 / kWaves, kBDma = kColBytes / 1024 / kWaves;
     constexpr bool kGateUp = FORM == kNT && EPI == kSwiglu;   // 128 gate + 128 up columns per tile
     constexpr int kTileCols = kGateUp ? kBN / 2 : kBN;        // output columns per tile
@@ -322,22 +352,27 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
 
     const int spp = (P.R + kBK - 1) / kBK;          // stages per pair
     const int nstages = spp * P.pairs;
-    const auto dma = [&](int s) {
+    const auto dma_a = [&](int s) {
         const int pair = FORM == kNN && s >= spp ? 1 : 0;
         const int r0 = (s - pair * spp) * kBK;
         const uint16_t* a = uniform_ptr((pair ? P.a1 : P.a0) + abase + r0);
-        const uint32_t buf = lds0 + (s % NS) * kStageBytes;
+        const uint32_t buf = lds0 + (s % NSA) * kRowBytes;
 #pragma unroll
         for (int i = 0; i < kADma; ++i) {
             const uint32_t vo = r0 + aunit[i] * 8 < P.R ? aoff[i] : kOutside;
             lds_dma16_buf(a, vo, buf + (i * kWaves + wave) * 1024);
         }
+    };
+    const auto dma_b = [&](int s) {
+        const int pair = FORM == kNN && s >= spp ? 1 : 0;
+        const int r0 = (s - pair * spp) * kBK;
+        const uint32_t buf = lds0 + kColRing + (s % NSB) * kColBytes;
 #pragma unroll
         for (int i = 0; i < kBDma; ++i) {
             const bool up = kGateUp && i >= kBDma / 2;
             const uint16_t* w = uniform_ptr((pair || up ? P.w1 : P.w0) + wbase + (FORM == kNT ? (int64_t)r0 : (int64_t)r0 * P.C));
             const bool ok = FORM == kNT ? r0 + bpos[i] * 8 < P.R : r0 + bpos[i] < P.R;
-            lds_dma16_buf(w, ok ? boff[i] : kOutside, buf + kRowBytes + (i * kWaves + wave) * 1024);
+            lds_dma16_buf(w, ok ? boff[i] : kOutside, buf + (i * kWaves + wave) * 1024);
         }
     };
 
@@ -361,50 +396,70 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
     for (int mi = 0; mi < U; ++mi)
 #pragma unroll
         for (int ni = 0; ni < kNI; ++ni) acc[mi][ni] = floatx4{0, 0, 0, 0};
-    run_stages<NS, U, kNI, kADma + kBDma, 1, FORM == kNT ? 1 : 2>(
-        nstages, dma,
-        [&](int buf, int ks, int mi) { return frag_rc((const lds_u8*)smem + buf * kStageBytes, aread[ks], 2 * mi); },
+    run_stages<NSA, NSB, U, kNI, kADma, kBDma, 1, FORM == kNT ? 1 : 2>(
+        nstages, dma_a, dma_b,
+        [&](int buf, int ks, int mi) { return frag_rc((const lds_u8*)smem + buf * kRowBytes, aread[ks], 2 * mi); },
         [&](int buf, int ks, int ni) {
-            const lds_u8* bs = (const lds_u8*)smem + buf * kStageBytes + kRowBytes;
+            const lds_u8* bs = (const lds_u8*)smem + kColRing + buf * kColBytes;
             if constexpr (FORM == kNT) return frag_rc(bs, bread[ks], kGateUp && ni >= 2 ? ni + 6 : ni);
             else return frag_ro<512>(bs, bread[ks] + bchunk[ni]);
         },
         acc);
 
-    // one rounding to bf16 per output
+    // One rounding to bf16 per output; a lane stores eight columns of one row.
+    // Every lane takes part in the exchanges, also those that store nothing.
+    constexpr int kPairs = kGateUp ? 1 : 2;
 #pragma unroll
     for (int mi = 0; mi < U; ++mi) {
         const int r = mi * 32 + wm * 16 + lrow;
-        if (r >= t.rows) continue;
         const int64_t row = (int64_t)(t.p0 + r) * P.C;
 #pragma unroll
-        for (int ni = 0; ni < (kGateUp ? 2 : kNI); ++ni) {
-            const int c = c0 + (kGateUp ? wn * 32 : wn * 64) + ni * 16 + q * 4;
-            if (c >= P.C) continue;
+        for (int j = 0; j < kPairs; ++j) {
+            const int c = c0 + (kGateUp ? wn * 32 : wn * 64 + j * 32) + (q & 1) * 16 + (q >> 1) * 8;
+            const bool ok = r < t.rows && c < P.C;
             if constexpr (kGateUp) {
-                const floatx4 a = acc[mi][ni], b = acc[mi][ni + 2];
-                floatx4 h;
+                floatx4 h[2];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) h[i] = silu(a[i]) * b[i];
-                store4(P.o0 + row + c, h);
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) h[n][i] = acc[mi][n][i] * sigmoid(acc[mi][n][i]) * acc[mi][n + 2][i];
+                const uint4 hv = pack_pair(h[0], h[1]);
+                if (ok) *reinterpret_cast<uint4*>(P.o0 + row + c) = hv;
                 if (P.o1) {
-                    store4(P.o1 + row + c, a);
-                    store4(P.o2 + row + c, b);
+                    const uint4 av = pack_pair(acc[mi][0], acc[mi][1]), bv = pack_pair(acc[mi][2], acc[mi][3]);
+                    if (ok) {
+                        *reinterpret_cast<uint4*>(P.o1 + row + c) = av;
+                        *reinterpret_cast<uint4*>(P.o2 + row + c) = bv;
+                    }
                 }
             } else if constexpr (EPI == kSwiglu) {
                 // dh = acc; da = dh b s (1 + a (1 - s)), db = dh a s, s = sigmoid(a)
-                const floatx4 a = load4(P.i0 + row + c), b = load4(P.i1 + row + c), dh = acc[mi][ni];
-                floatx4 da, db;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float sg = 1.0f / (1.0f + __expf(-a[i]));
-                    db[i] = dh[i] * a[i] * sg;
-                    da[i] = dh[i] * b[i] * (sg + a[i] * sg * (1.0f - sg));
+                uint4 av = make_uint4(0, 0, 0, 0), bv = av;
+                if (ok) {
+                    av = *reinterpret_cast<const uint4*>(P.i0 + row + c);
+                    bv = *reinterpret_cast<const uint4*>(P.i1 + row + c);
                 }
-                store4(P.o0 + row + c, da);
-                store4(P.o1 + row + c, db);
+                const Pair4 ap = exchange_back(av), bp = exchange_back(bv);
+                const floatx4 a[2] = {widen4(ap.a0, ap.a1), widen4(ap.b0, ap.b1)};
+                const floatx4 b[2] = {widen4(bp.a0, bp.a1), widen4(bp.b0, bp.b1)};
+                floatx4 da[2], db[2];
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float dh = acc[mi][2 * j + n][i], sg = sigmoid(a[n][i]), act = a[n][i] * sg;
+                        db[n][i] = dh * act;
+                        da[n][i] = dh * b[n][i] * (sg + act * (1.0f - sg));
+                    }
+                av = pack_pair(da[0], da[1]);
+                bv = pack_pair(db[0], db[1]);
+                if (ok) {
+                    *reinterpret_cast<uint4*>(P.o0 + row + c) = av;
+                    *reinterpret_cast<uint4*>(P.o1 + row + c) = bv;
+                }
             } else {
-                store4(P.o0 + row + c, acc[mi][ni]);
+                const uint4 v = pack_pair(acc[mi][2 * j], acc[mi][2 * j + 1]);
+                if (ok) *reinterpret_cast<uint4*>(P.o0 + row + c) = v;
             }
         }
     }
@@ -412,21 +467,22 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
 
 // Tiles of up to BM rows, by their rows: a short tile waits for memory, not
 // for the matrix units, and its smaller stages leave room for more of them in
-// flight (2 to 4 of 64 to 40 KB in 160 KB of LDS).  BM == 64: two workgroups a CU instead.
+// flight.  The weights, which come from HBM, have a stage more in flight than
+// the rows, which come from L2.  BM == 64: two workgroups a CU instead.
 template <int FORM, int EPI, int BM>
 __global__ void __launch_bounds__(kThreads, BM == 64 ? 4 : 2) k_rows_mm(MmParams P) {
     extern __shared__ __align__(16) uint8_t smem[];
-    constexpr int NS64 = BM == 64 ? 2 : 4;
+    constexpr int N64 = BM == 64 ? 2 : 4;
     const RowTile t = find_tile<BM>(P, blockIdx.x);
     if (t.e < 0) return;
-    if (t.rows <= 32) rows_tile<FORM, EPI, 64, 1, NS64>(P, t, smem);
-    else if (BM == 64 || t.rows <= 64) rows_tile<FORM, EPI, 64, 2, NS64>(P, t, smem);
+    if (t.rows <= 32) rows_tile<FORM, EPI, 64, 1, N64, N64>(P, t, smem);
+    else if (BM == 64 || t.rows <= 64) rows_tile<FORM, EPI, 64, 2, N64, N64>(P, t, smem);
     else if constexpr (BM > 64) {
-        if (t.rows <= 96) rows_tile<FORM, EPI, 128, 3, 3>(P, t, smem);
-        else if (t.rows <= 128) rows_tile<FORM, EPI, 128, 4, 3>(P, t, smem);
-        else if (t.rows <= 160) rows_tile<FORM, EPI, 192, 5, 2>(P, t, smem);
-        else if (t.rows <= 192) rows_tile<FORM, EPI, 192, 6, 2>(P, t, smem);
-        else rows_tile<FORM, EPI, 256, 8, 2>(P, t, smem);
+        if (t.rows <= 96) rows_tile<FORM, EPI, 128, 3, 3, 3>(P, t, smem);
+        else if (t.rows <= 128) rows_tile<FORM, EPI, 128, 4, 3, 3>(P, t, smem);
+        else if (t.rows <= 160) rows_tile<FORM, EPI, 192, 5, 2, 3>(P, t, smem);
+        else if (t.rows <= 192) rows_tile<FORM, EPI, 192, 6, 2, 3>(P, t, smem);
+        else rows_tile<FORM, EPI, 256, 8, 2, 3>(P, t, smem);
     }
 }
 
@@ -489,14 +545,18 @@ __global__ void __launch_bounds__(kThreads, MI * NI <= 8 ? 4 : 2) k_wgrad(WgradP
 #pragma unroll
         for (int i = 0; i < kBDma; ++i) slot[i] = P.slots[min(p0 + s * kBK + xrow[i], P.M - 1)];
     };
-    const auto dma = [&](int s) {
+    const auto dma_a = [&](int s) {
         const int r0 = s * kBK;
         const uint32_t buf = lds0 + (s % NS) * kStageBytes;
         const uint16_t* a = uniform_ptr(P.dy + (int64_t)(p0 + r0) * P.N + n0);
-        const uint16_t* x = uniform_ptr(P.x + (P.slots ? 0 : (int64_t)(p0 + r0) * P.K) + k0);
 #pragma unroll
         for (int i = 0; i < kADma; ++i)
             lds_dma16_buf(a, r0 + arow[i] < cnt ? aoff[i] : kOutside, buf + (i * kWaves + wave) * 1024);
+    };
+    const auto dma_b = [&](int s) {
+        const int r0 = s * kBK;
+        const uint32_t buf = lds0 + (s % NS) * kStageBytes;
+        const uint16_t* x = uniform_ptr(P.x + (P.slots ? 0 : (int64_t)(p0 + r0) * P.K) + k0);
 #pragma unroll
         for (int i = 0; i < kBDma; ++i) {
             int src = xrow[i];
@@ -532,8 +592,8 @@ __global__ void __launch_bounds__(kThreads, MI * NI <= 8 ? 4 : 2) k_wgrad(WgradP
 
     load_slots(0);
     if (nstages > 0)
-        run_stages<NS, MI, NI, kADma + kBDma, 2, 2>(
-            nstages, dma,
+        run_stages<NS, NS, MI, NI, kADma, kBDma, 2, 2>(
+            nstages, dma_a, dma_b,
             [&](int buf, int ks, int mi) {
                 return frag_ro<TM * 2>((const lds_u8*)smem + buf * kStageBytes, ard[ks] + ac[mi]);
             },
@@ -599,7 +659,8 @@ int64_t row_tiles_bound(int M, int E, int BM) { return M / BM + (int64_t)std::mi
 template <int FORM, int EPI, int BM>
 moe_status launch_rows(const MmParams& P, const char* name, hipStream_t s) {
     const int64_t grid = xcd_grid(row_tiles_bound(P.M, P.E, BM) * P.ntc);
-    const size_t lds = BM == 64 ? rows_lds(64, 2) : std::max({rows_lds(64, 4), rows_lds(128, 3), rows_lds(256, 2)});
+    const size_t lds = BM == 64 ? rows_lds(64, 2, 2) : rows_lds(256, 2, 3);
+    static_assert(rows_lds(256, 2, 3) >= rows_lds(64, 4, 4) && rows_lds(256, 2, 3) >= rows_lds(128, 3, 3), "one size");
     moe_status st = allow_dynamic_lds(reinterpret_cast<const void*>(&k_rows_mm<FORM, EPI, BM>), lds);
     if (st != MOE_OK) return st;
     MOE_LAUNCH(name, (k_rows_mm<FORM, EPI, BM>), dim3((unsigned)grid), dim3(kThreads), lds, s, P);
