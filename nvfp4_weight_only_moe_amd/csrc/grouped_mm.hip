@@ -143,6 +143,48 @@ __device__ __forceinline__ void run_stages(int nstages, DmaA&& dma_a, DmaB&& dma
     }
 }
 
+// The same with stages of one k-step and one ring of NS buffers (each holds
+// both operands): while a stage's MFMAs run, the next one is read.
+template <int NS, int U, int NI, int OPS, int READS_A, int READS_B, class Dma, class ReadA, class ReadB, class Acc>
+__device__ __forceinline__ void run_steps(int nstages, Dma&& dma, ReadA&& ra, ReadB&& rb, Acc& acc) {
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+        if (i < nstages) dma(i);
+    wait_stages_behind<OPS>(min(NS, nstages) - 1);
+    wait_lds_barrier();
+    bf16x8 af[U], b0[NI], b1[NI];
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni) b0[ni] = rb(0, ni);
+#pragma unroll
+    for (int mi = 0; mi < U; ++mi) af[mi] = ra(0, mi);
+    int buf = 0;
+    const auto step = [&](int s, bf16x8 (&now)[NI], bf16x8 (&then)[NI]) {
+        wait_stages_behind<OPS>(min(NS - 2, nstages - 2 - s));   // stage s + 1 is in LDS
+        wait_lds_barrier();                                      // and stage s has been read
+        if (s + NS < nstages) dma(s + NS);
+        buf = buf + 1 == NS ? 0 : buf + 1;
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni) then[ni] = rb(buf, ni);
+#pragma unroll
+        for (int mi = 0; mi < U; ++mi) {
+#pragma unroll
+            for (int ni = 0; ni < NI; ++ni)
+                acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(now[ni], af[mi], acc[mi][ni], 0, 0, 0);
+            af[mi] = ra(buf, mi);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x100, NI * READS_B, 0);
+#pragma unroll
+        for (int mi = 0; mi < U; ++mi) {
+            __builtin_amdgcn_sched_group_barrier(0x008, NI, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, READS_A, 0);
+        }
+    };
+    for (int s = 0; s < nstages; s += 2) {
+        step(s, b0, b1);
+        if (s + 1 < nstages) step(s + 1, b1, b0);
+    }
+}
+
 struct MmParams {
     const uint16_t* a0;           // row operand: x, or dy
     const uint16_t* a1;           // NN: the second pair's dy, or null
@@ -438,14 +480,22 @@ struct WgradParams {
     int parts;                    // how many fit (offsets that are not ascending could ask for more)
 };
 
-// One workgroup: a tile of 32 MI x 64 NI of one expert's dW over one slice of its rows.
-template <int MI, int NI, int NS>
-__global__ void __launch_bounds__(kThreads, MI * NI <= 8 ? 4 : 2) k_wgrad(WgradParams P) {
-    constexpr int TM = MI * 32, TN = NI * 64;                       // rows n, columns k of the tile
-    constexpr int kABytes = TM * kBK * 2, kBBytes = TN * kBK * 2, kStageBytes = kABytes + kBBytes;
-    constexpr int kADma = kABytes / 1024 / kWaves, kBDma = kBBytes / 1024 / kWaves;
+constexpr int kSrcRows = 1024;    // gathered rows whose places in x are kept in LDS at a time
+
+constexpr int wgrad_lds(int W, int MI, int NI, int BK, int NS) {
+    return NS * (MI * (W / 4) * 16 + NI * 64) * BK * 2 + kSrcRows * 4;
+}
+
+// One workgroup of W waves, W / 4 along n by 4 along k: a tile of 4 W MI x
+// 64 NI of one expert's dW over one slice of its rows, in stages of BK rows.
+template <int W, int MI, int NI, int BK, int NS>
+__global__ void __launch_bounds__(W * kWave, 2) k_wgrad(WgradParams P) {
+    constexpr int TM = W / 4 * MI * 16, TN = NI * 64;               // rows n, columns k of the tile
+    constexpr int kABytes = TM * BK * 2, kBBytes = TN * BK * 2, kStageBytes = kABytes + kBBytes;
+    constexpr int kADma = kABytes / 1024 / W, kBDma = kBBytes / 1024 / W;
     constexpr int kARows = 512 / TM, kBRows = 512 / TN;             // LDS rows per DMA
     extern __shared__ __align__(16) uint8_t smem[];
+    uint32_t* srcs = reinterpret_cast<uint32_t*>(smem + NS * kStageBytes);
     const int per = P.ntn * P.ntk;
     const Piece f = find_piece<true>(P.offsets, P.E, P.M, P.slice, per, blockIdx.x);
     if (f.e < 0) return;
@@ -460,57 +510,57 @@ __global__ void __launch_bounds__(kThreads, MI * NI <= 8 ? 4 : 2) k_wgrad(WgradP
 
     // a lane's LDS row and the columns that it fetches, per DMA
     uint32_t aoff[kADma], xcol[kBDma];
-    int arow[kADma], xrow[kBDma], slot[kBDma];
+    int arow[kADma], xrow[kBDma];
     const auto column = [&](int r, int pos) { return (((pos >> 1) ^ ro_swizzle(r)) << 4) + ((pos & 1) << 3); };
 #pragma unroll
     for (int i = 0; i < kADma; ++i) {
-        const int r = (i * kWaves + wave) * kARows + lane / (64 / kARows), col = column(r, lane % (64 / kARows));
+        const int r = (i * W + wave) * kARows + lane / (64 / kARows), col = column(r, lane % (64 / kARows));
         arow[i] = r;
         aoff[i] = n0 + col < P.N ? (uint32_t)r * (uint32_t)P.N * 2u + col * 2 : kOutside;
     }
 #pragma unroll
     for (int i = 0; i < kBDma; ++i) {
-        const int r = (i * kWaves + wave) * kBRows + lane / (64 / kBRows), col = column(r, lane % (64 / kBRows));
+        const int r = (i * W + wave) * kBRows + lane / (64 / kBRows), col = column(r, lane % (64 / kBRows));
         xrow[i] = r;
         xcol[i] = k0 + col < P.K ? (uint32_t)col * 2u : kOutside;
-        slot[i] = 0;
     }
-    const int nstages = (cnt + kBK - 1) / kBK;
-    const auto load_slots = [&](int s) {
-        if (!P.slots) return;
-#pragma unroll
-        for (int i = 0; i < kBDma; ++i) slot[i] = P.slots[min(p0 + s * kBK + xrow[i], P.M - 1)];
+    const int nstages = (cnt + BK - 1) / BK;
+    // Gathered: the byte offsets in x of the next kSrcRows rows (kOutside:
+    // none), looked up ahead of the stages, since a load in line with their
+    // DMAs would wait for all of them.
+    const auto look_up = [&](int s) {
+        for (int i = threadIdx.x; i < kSrcRows; i += W * kWave) {
+            const int r = s * BK + i, slot = P.slots[min(p0 + r, P.M - 1)], src = slot_token(slot, P.k, P.kmagic);
+            srcs[i] = r < cnt && slot >= 0 && src < P.X ? (uint32_t)src * (uint32_t)P.K * 2u : kOutside;
+        }
+        wait_lds_barrier();
     };
     const auto dma_a = [&](int s) {
-        const int r0 = s * kBK;
+        const int r0 = s * BK;
         const uint32_t buf = lds0 + (s % NS) * kStageBytes;
         const uint16_t* a = uniform_ptr(P.dy + (int64_t)(p0 + r0) * P.N + n0);
 #pragma unroll
         for (int i = 0; i < kADma; ++i)
-            lds_dma16_buf(a, r0 + arow[i] < cnt ? aoff[i] : kOutside, buf + (i * kWaves + wave) * 1024);
+            lds_dma16_buf(a, r0 + arow[i] < cnt ? aoff[i] : kOutside, buf + (i * W + wave) * 1024);
     };
     const auto dma_b = [&](int s) {
-        const int r0 = s * kBK;
+        const int r0 = s * BK;
         const uint32_t buf = lds0 + (s % NS) * kStageBytes;
+        if (P.slots && r0 % kSrcRows == 0) look_up(s);
         const uint16_t* x = uniform_ptr(P.x + (P.slots ? 0 : (int64_t)(p0 + r0) * P.K) + k0);
 #pragma unroll
         for (int i = 0; i < kBDma; ++i) {
-            int src = xrow[i];
-            bool ok = r0 + xrow[i] < cnt && xcol[i] != kOutside;
-            if (P.slots) {
-                src = slot_token(slot[i], P.k, P.kmagic);
-                ok = ok && slot[i] >= 0 && src < P.X;
-            }
-            lds_dma16_buf(x, ok ? (uint32_t)src * (uint32_t)P.K * 2u + xcol[i] : kOutside,
-                          buf + kABytes + (i * kWaves + wave) * 1024);
+            const uint32_t row = P.slots ? srcs[(r0 + xrow[i]) % kSrcRows]
+                                         : r0 + xrow[i] < cnt ? (uint32_t)xrow[i] * (uint32_t)P.K * 2u : kOutside;
+            lds_dma16_buf(x, row != kOutside && xcol[i] != kOutside ? row + xcol[i] : kOutside,
+                          buf + kABytes + (i * W + wave) * 1024);
         }
-        load_slots(s + 1);                          // for the next call
     };
 
-    int ard[2], brd[2], ac[MI], bc[NI];
+    int ard[BK / 32], brd[BK / 32], ac[MI], bc[NI];
     const int sw = (lrow >> 2) | ((q & 1) << 2);
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
+    for (int ks = 0; ks < BK / 32; ++ks) {
         const int r = ks * 32 + q * 8 + (lrow >> 2);
         ard[ks] = r * TM * 2 + (lrow & 3) * 8;
         brd[ks] = r * TN * 2 + (lrow & 3) * 8;
@@ -526,35 +576,50 @@ __global__ void __launch_bounds__(kThreads, MI * NI <= 8 ? 4 : 2) k_wgrad(WgradP
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = floatx4{0, 0, 0, 0};
 
-    load_slots(0);
-    if (nstages > 0)
-        run_stages<NS, NS, MI, NI, kADma, kBDma, 2, 2>(
-            nstages, dma_a, dma_b,
-            [&](int buf, int ks, int mi) {
-                return frag_ro<TM * 2>((const lds_u8*)smem + buf * kStageBytes, ard[ks] + ac[mi]);
-            },
-            [&](int buf, int ks, int ni) {
-                return frag_ro<TN * 2>((const lds_u8*)smem + buf * kStageBytes + kABytes, brd[ks] + bc[ni]);
-            },
-            acc);
+    const auto read_a = [&](int buf, int ks, int mi) {
+        return frag_ro<TM * 2>((const lds_u8*)smem + buf * kStageBytes, ard[ks] + ac[mi]);
+    };
+    const auto read_b = [&](int buf, int ks, int ni) {
+        return frag_ro<TN * 2>((const lds_u8*)smem + buf * kStageBytes + kABytes, brd[ks] + bc[ni]);
+    };
+    if (nstages > 0) {
+        if constexpr (BK == 64)
+            run_stages<NS, NS, MI, NI, kADma, kBDma, 2, 2>(nstages, dma_a, dma_b, read_a, read_b, acc);
+        else
+            run_steps<NS, MI, NI, kADma + kBDma, 2, 2>(
+                nstages, [&](int s) { dma_a(s); dma_b(s); }, [&](int buf, int mi) { return read_a(buf, 0, mi); },
+                [&](int buf, int ni) { return read_b(buf, 0, ni); }, acc);
+    }
     const bool whole = f.pieces == 1;
     if (!whole && f.cut_before + sl >= P.parts) return;
     float* base = whole ? P.dw + (int64_t)e * P.N * P.K : P.part + (int64_t)(f.cut_before + sl) * P.N * P.K;
     const bool add = whole && P.accumulate;
+    // Lanes l and l + 8 of 16 trade a subtile, so that a store instruction
+    // writes 128 bytes of eight rows and not 64 of sixteen.
+    const bool upper = lrow & 8;
 #pragma unroll
-    for (int mi = 0; mi < MI; ++mi) {
-        const int n = n0 + (wm * MI + mi) * 16 + lrow;
-        if (n >= P.N) continue;
-        float* row = base + (int64_t)n * P.K;
+    for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
-        for (int ni = 0; ni < NI; ++ni) {
-            const int c = k0 + (wn * NI + ni) * 16 + q * 4;
-            if (c >= P.K) continue;
-            floatx4 v = acc[mi][ni];
-            if (add) v += *reinterpret_cast<const floatx4*>(row + c);
-            *reinterpret_cast<floatx4*>(row + c) = v;
+        for (int j = 0; j < NI / 2; ++j) {
+            const floatx4 u = acc[mi][2 * j], v = acc[mi][2 * j + 1];
+            floatx4 lo, hi;                             // rows 0 .. 7, rows 8 .. 15 of the subtile
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float tu = dpp_f32<0x128>(0.0f, u[i]), tv = dpp_f32<0x128>(0.0f, v[i]);
+                lo[i] = upper ? tv : u[i];
+                hi[i] = upper ? v[i] : tu;
+            }
+            const int c = k0 + (wn * NI + 2 * j + (lrow >> 3)) * 16 + q * 4;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int n = n0 + (wm * MI + mi) * 16 + h * 8 + (lrow & 7);
+                if (n >= P.N || c >= P.K) continue;
+                floatx4 w = h ? hi : lo;
+                floatx4* p = reinterpret_cast<floatx4*>(base + (int64_t)n * P.K + c);
+                if (add) w += *p;
+                __builtin_nontemporal_store(w, p);
+            }
         }
-    }
 }
 
 // dW of the experts whose rows were cut into slices: the slices' sums, in order.
@@ -617,16 +682,22 @@ struct WgradPlan {
 
 WgradPlan wgrad_plan(int M, int N, int K, int E) {
     WgradPlan p{};
-    const int64_t big_tiles = (int64_t)((N + 255) / 256) * ((K + 255) / 256) * E;
-    p.big = big_tiles >= 256;
-    const int T = p.big ? 256 : 128;
-    p.ntn = (N + T - 1) / T;
-    p.ntk = (K + T - 1) / T;
+    p.ntk = (K + 255) / 256;
+    // the tile of 256 n reads x half as often; the one of 128 leaves room for
+    // two workgroups a CU, better with few rows (32 experts, 1536 x 5120: 16
+    // rows 193 us against 206, 256 rows 321 against 310), and wastes less on a small N
+    p.big = M / E >= 192 && (N + 127) / 128 % 2 == 0;
+    const int TM = p.big ? 256 : 128;
+    p.ntn = (N + TM - 1) / TM;
     const int64_t per = (int64_t)p.ntn * p.ntk, slots = p.big ? 256 : 512;
     p.slice = 1 << 30;
-    if (per * E < slots) {
-        const int64_t want = std::max<int64_t>(1, slots / per), stages = (M + kBK - 1) / kBK;
-        const int64_t rows = std::max<int64_t>((stages + want - 1) / want, 4) * kBK;
+    // Few tiles: slices, so that their number comes near the workgroups that
+    // run at once.  Not under 16 stages with several experts (the join and its
+    // partial sums cost as much as 10 to 20 stages, and only a long expert is
+    // then cut at all), 8 with one, whose rows are known.
+    if (2 * per * E <= slots) {
+        const int64_t want = slots / per, stages = (M + kBK - 1) / kBK;
+        const int64_t rows = std::max<int64_t>((stages + want - 1) / want, E == 1 ? 8 : 16) * kBK;
         if (rows < M) p.slice = (int)rows;
     }
     p.parts = p.slice < M ? 2 * (M / p.slice) + 2 : 0;
@@ -635,12 +706,13 @@ WgradPlan wgrad_plan(int M, int N, int K, int E) {
     return p;
 }
 
-template <int MI, int NI, int NS>
+template <int W, int MI, int NI, int BK, int NS>
 moe_status launch_wgrad(const WgradParams& P, int64_t tiles, hipStream_t s) {
-    const size_t lds = NS * (MI * 32 + NI * 64) * kBK * 2;
-    moe_status st = allow_dynamic_lds(reinterpret_cast<const void*>(&k_wgrad<MI, NI, NS>), lds);
+    constexpr size_t lds = wgrad_lds(W, MI, NI, BK, NS);
+    moe_status st = allow_dynamic_lds(reinterpret_cast<const void*>(&k_wgrad<W, MI, NI, BK, NS>), lds);
     if (st != MOE_OK) return st;
-    MOE_LAUNCH("grouped_wgrad", (k_wgrad<MI, NI, NS>), dim3((unsigned)xcd_grid(tiles)), dim3(kThreads), lds, s, P);
+    MOE_LAUNCH("grouped_wgrad", (k_wgrad<W, MI, NI, BK, NS>), dim3((unsigned)xcd_grid(tiles)), dim3(W * kWave), lds, s,
+               P);
     return MOE_OK;
 }
 
@@ -710,7 +782,7 @@ moe_status launch_grouped_wgrad(const GroupedArgs& g, float* dw, bool accumulate
     P.dw = dw;
     P.part = static_cast<float*>(ws);
     P.parts = p.parts;
-    const moe_status st = p.big ? launch_wgrad<8, 4, 2>(P, p.tiles, s) : launch_wgrad<4, 2, 2>(P, p.tiles, s);
+    const moe_status st = p.big ? launch_wgrad<8, 8, 4, 64, 2>(P, p.tiles, s) : launch_wgrad<4, 8, 4, 32, 3>(P, p.tiles, s);
     if (st != MOE_OK || p.part_bytes == 0) return st;
     MOE_LAUNCH("grouped_wgrad_join", k_wgrad_join, dim3((unsigned)(((int64_t)g.N * g.K + 1023) / 1024), g.E), dim3(256),
                0, s, P);
