@@ -13,8 +13,8 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kCols = kThreads * 8;       // columns per pass of a workgroup
+constexpr int kMaxThreads = 512;
+constexpr int kSlots = 8;                 // slots whose rows are loaded together
 
 __device__ __forceinline__ void widen8(uint4 v, float (&f)[8]) {
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
@@ -32,24 +32,46 @@ __device__ __forceinline__ uint4 narrow8(const float (&f)[8]) {
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-__global__ void __launch_bounds__(kThreads) k_combine_rows(const uint16_t* __restrict__ y, int M, int H,
-                                                           const int32_t* __restrict__ pos,
-                                                           const float* __restrict__ w, int k,
-                                                           uint16_t* __restrict__ out) {
+__device__ __forceinline__ uint4 load_row(const uint16_t* p) { return load_stream16(reinterpret_cast<const uint4*>(p)); }
+__device__ __forceinline__ void store_row(uint16_t* p, uint4 v) {
+    __builtin_nontemporal_store(nt_u32x4{v.x, v.y, v.z, v.w}, reinterpret_cast<nt_u32x4*>(p));
+}
+
+// One workgroup per token, eight columns a thread and pass.  HBM-bound: the
+// rows of eight slots are requested before any is used (a dropped slot reads
+// row 0 and drops it: no branch between the loads), past the caches, since each
+// is used once.  4099 tokens, 8 slots of 5120: 79.7 us with the loads in a loop
+// over the slots, 67.8 us so (378 MB: 5.6 TB/s; a copy reaches 5.1).
+__global__ void __launch_bounds__(kMaxThreads) k_combine_rows(const uint16_t* __restrict__ y, int M, int H,
+                                                              const int32_t* __restrict__ pos,
+                                                              const float* __restrict__ w, int k,
+                                                              uint16_t* __restrict__ out) {
     const int64_t t = blockIdx.x;
-    const int c = (blockIdx.y * kThreads + threadIdx.x) * 8;
-    if (c >= H) return;
-    float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int j = 0; j < k; ++j) {
-        const int p = pos[t * k + j];
-        if ((unsigned)p >= (unsigned)M) continue;
-        const float wj = w ? w[t * k + j] : 1.0f;
-        float f[8];
-        widen8(*reinterpret_cast<const uint4*>(y + (int64_t)p * H + c), f);
+    for (int c = threadIdx.x * 8; c < H; c += blockDim.x * 8) {
+        float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int j0 = 0; M > 0 && j0 < k; j0 += kSlots) {
+            uint4 v[kSlots];
+            float wj[kSlots];
+            bool ok[kSlots];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = fmaf(wj, f[i], acc[i]);
+            for (int j = 0; j < kSlots; ++j) {
+                const int64_t s = t * k + min(j0 + j, k - 1);
+                const int p = pos[s];
+                ok[j] = j0 + j < k && (unsigned)p < (unsigned)M;
+                wj[j] = w ? w[s] : 1.0f;
+                v[j] = load_row(y + (int64_t)(ok[j] ? p : 0) * H + c);
+            }
+#pragma unroll
+            for (int j = 0; j < kSlots; ++j) {
+                if (!ok[j]) continue;                     // the same for the whole workgroup
+                float f[8];
+                widen8(v[j], f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[i] = fmaf(wj[j], f[i], acc[i]);
+            }
+        }
+        *reinterpret_cast<uint4*>(out + t * H + c) = narrow8(acc);
     }
-    *reinterpret_cast<uint4*>(out + t * H + c) = narrow8(acc);
 }
 
 struct CombineBwd {
@@ -64,39 +86,67 @@ struct CombineBwd {
     float* dlogits;
 };
 
-// One workgroup per token: dout's row is read once and meets the k rows.
-__global__ void __launch_bounds__(kThreads) k_combine_bwd(CombineBwd P) {
-    __shared__ float s_part[kThreads / kWave][MOE_MAX_TOPK];
+// One workgroup per token: a piece of dout's row meets the rows of eight
+// slots at a time (requested together, as above), whose dy rows leave at once
+// (2048 tokens, 8 slots of 5120: 84 -> 72 us, 5.0 TB/s).
+template <bool DOT>
+__global__ void __launch_bounds__(kMaxThreads) k_combine_bwd(CombineBwd P) {
+    __shared__ float s_part[kMaxThreads / kWave][MOE_MAX_TOPK];
     __shared__ float s_dw[MOE_MAX_TOPK], s_g[MOE_MAX_TOPK];
     __shared__ int s_id[MOE_MAX_TOPK];
     const int64_t t = blockIdx.x;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int j = 0; j < P.k; ++j) {
-        const int p = P.pos[t * P.k + j];
-        const bool ok = (unsigned)p < (unsigned)P.M;
-        const float wj = P.w ? P.w[t * P.k + j] : 1.0f;
-        float dot = 0.0f;
-        for (int c = threadIdx.x * 8; ok && c < P.H; c += kCols) {
-            float d[8], o[8];
-            widen8(*reinterpret_cast<const uint4*>(P.dout + t * P.H + c), d);
-            if (P.dw || P.dlogits) {
-                float f[8];
-                widen8(*reinterpret_cast<const uint4*>(P.y + (int64_t)p * P.H + c), f);
+    for (int j0 = 0; j0 < P.k; j0 += kSlots) {
+        int64_t row[kSlots];
+        float wj[kSlots], dot[kSlots];
+        bool ok[kSlots];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) dot = fmaf(d[i], f[i], dot);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = wj * d[i];
-            *reinterpret_cast<uint4*>(P.dy + (int64_t)p * P.H + c) = narrow8(o);
+        for (int j = 0; j < kSlots; ++j) {
+            const int64_t s = t * P.k + min(j0 + j, P.k - 1);
+            const int p = P.pos[s];
+            ok[j] = j0 + j < P.k && (unsigned)p < (unsigned)P.M;
+            wj[j] = P.w ? P.w[s] : 1.0f;
+            row[j] = (int64_t)(ok[j] ? p : 0) * P.H;
+            dot[j] = 0.0f;
         }
-        dot = wave_sum_dpp(dot);
-        if (lane == 0) s_part[wave][j] = dot;
+        for (int c = threadIdx.x * 8; c < P.H; c += blockDim.x * 8) {
+            const uint4 dv = *reinterpret_cast<const uint4*>(P.dout + t * P.H + c);
+            uint4 v[kSlots];
+            if constexpr (DOT) {
+                if (P.M > 0)
+#pragma unroll
+                    for (int j = 0; j < kSlots; ++j) v[j] = load_row(P.y + row[j] + c);
+            }
+            float d[8];
+            widen8(dv, d);
+#pragma unroll
+            for (int j = 0; j < kSlots; ++j) {
+                if (!ok[j]) continue;                     // the same for the whole workgroup
+                float o[8];
+                if constexpr (DOT) {
+                    float f[8];
+                    widen8(v[j], f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) dot[j] = fmaf(d[i], f[i], dot[j]);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = wj[j] * d[i];
+                store_row(P.dy + row[j] + c, narrow8(o));
+            }
+        }
+        if constexpr (DOT) {
+#pragma unroll
+            for (int j = 0; j < kSlots; ++j) {
+                const float sum = wave_sum_dpp(dot[j]);
+                if (lane == 0 && j0 + j < P.k) s_part[wave][j0 + j] = sum;
+            }
+        }
     }
-    if (!P.dw && !P.dlogits) return;
+    if constexpr (!DOT) return;
     __syncthreads();
     if ((int)threadIdx.x < P.k) {
         float v = 0.0f;
-        for (int i = 0; i < kThreads / kWave; ++i) v += s_part[i][threadIdx.x];
+        for (int i = 0; i < (int)blockDim.x / kWave; ++i) v += s_part[i][threadIdx.x];
         s_dw[threadIdx.x] = v;
         if (P.dw) P.dw[t * P.k + threadIdx.x] = v;
     }
@@ -109,19 +159,24 @@ __global__ void __launch_bounds__(kThreads) k_combine_bwd(CombineBwd P) {
         s_id[threadIdx.x] = P.ids[t * P.k + threadIdx.x];
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < P.E; e += kThreads) {
+    for (int e = threadIdx.x; e < P.E; e += blockDim.x) {
         float v = 0.0f;
         for (int j = 0; j < P.k; ++j) v += s_id[j] == e ? s_g[j] : 0.0f;
         P.dlogits[t * P.E + e] = v;
     }
 }
 
+// Threads of a workgroup: whole waves, H / 8 shared out over as few equal passes as 512 allow.
+dim3 row_threads(int H) {
+    const int passes = (H / 8 + kMaxThreads - 1) / kMaxThreads;
+    return dim3(((H / 8 + passes - 1) / passes + kWave - 1) / kWave * kWave);
+}
+
 }  // namespace
 
 moe_status launch_combine_rows(const uint16_t* y, int M, int H, const int32_t* pos, const float* w, int T, int k,
                                uint16_t* out, hipStream_t s) {
-    MOE_LAUNCH("combine_rows", k_combine_rows, dim3(T, (H + kCols - 1) / kCols), dim3(kThreads), 0, s, y, M, H, pos, w,
-               k, out);
+    MOE_LAUNCH("combine_rows", k_combine_rows, dim3(T), row_threads(H), 0, s, y, M, H, pos, w, k, out);
     return MOE_OK;
 }
 
@@ -129,7 +184,8 @@ moe_status launch_combine_bwd(const uint16_t* dout, const uint16_t* y, const int
                               const int32_t* ids, int T, int M, int H, int k, int E, uint16_t* dy, float* dw,
                               float* dlogits, hipStream_t s) {
     CombineBwd P{dout, y, pos, w, ids, M, H, k, E, dy, dw, dlogits};
-    MOE_LAUNCH("combine_bwd", k_combine_bwd, dim3(T), dim3(kThreads), 0, s, P);
+    if (dw || dlogits) MOE_LAUNCH("combine_bwd", k_combine_bwd<true>, dim3(T), row_threads(H), 0, s, P);
+    else MOE_LAUNCH("combine_bwd", k_combine_bwd<false>, dim3(T), row_threads(H), 0, s, P);
     return MOE_OK;
 }
 

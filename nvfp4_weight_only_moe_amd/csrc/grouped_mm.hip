@@ -30,13 +30,11 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 512;             // 8 waves: 2 along the rows x 4 along the columns
-constexpr int kWaves = kThreads / kWave;
 constexpr int kBN = 256;                  // output columns per tile, 64 per wave
 constexpr int kNI = 4;                    // 16-column subtiles per wave
 constexpr int kBK = 64;                   // reduction steps per stage
 constexpr uint32_t kOutside = 0xFFFFFFFFu;
 constexpr uint32_t kRecords = 0xFFFFFF00u;   // descriptor size: every real offset is below it
-constexpr int kColBytes = kBN * kBK * 2;
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -211,7 +209,7 @@ struct RowTile {
 // tiles after each other.
 template <int BM>
 __device__ __forceinline__ RowTile find_tile(const MmParams& P, int bid) {
-    const Piece f = find_piece<false>(P.offsets, P.E, P.M, BM, P.ntc, bid);
+    const Piece f = find_piece<false, BM * 5 / 8>(P.offsets, P.E, P.M, BM, P.ntc, bid);
     if (f.e < 0) return RowTile{-1, 0, 0, 0};
     const int full = f.pieces / kMGroup * kMGroup;
     int m, c;
@@ -232,9 +230,13 @@ __device__ __forceinline__ RowTile find_tile(const MmParams& P, int bid) {
 
 // ---- fragments: lane l holds output position l & 15, reduction steps
 // 8 (l >> 4) .. + 7 of the k-step
+template <int BK>                           // reduction steps of an LDS row
 __device__ __forceinline__ bf16x8 frag_rc(const lds_u8* tile, int lane_off, int sub) {
-    return *reinterpret_cast<const __attribute__((address_space(3))) bf16x8*>(tile + lane_off + sub * 2048);
+    return *reinterpret_cast<const __attribute__((address_space(3))) bf16x8*>(tile + lane_off + sub * (BK * 32));
 }
+// LDS unit (16 bytes) of unit u of row r
+template <int BK>
+__device__ __forceinline__ int rc_swizzle(int r) { return BK == 64 ? (r >> 1) & 7 : (r >> 2) & 3; }
 template <int ROW>                          // bytes of an LDS row
 __device__ __forceinline__ bf16x8 frag_ro(const lds_u8* tile, int lane_off) {
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + lane_off));
@@ -275,14 +277,18 @@ __device__ __forceinline__ floatx4 widen4(uint32_t lo, uint32_t hi) {
                    __uint_as_float(hi & 0xFFFF0000u)};
 }
 
-constexpr int rows_lds(int BM, int NSA, int NSB) { return NSA * BM * kBK * 2 + NSB * kColBytes; }
+constexpr int rows_lds(int BM, int BK, int NSA, int NSB) { return (NSA * BM + NSB * kBN) * BK * 2; }
 
-// One tile: U of each wave's BM / 32 16-row subtiles.  The two waves of a SIMD
-// take the tile's subtiles in turn, so a short tile costs both the same.
-template <int FORM, int EPI, int BM, int U, int NSA, int NSB>
+// One tile of up to BM rows by 256 columns on W waves, W / 4 along the rows by
+// 4 along the columns, in stages of BK reduction steps: U 16-row subtiles a
+// wave.  The two waves of a SIMD (W == 8) take the tile's subtiles in turn, so
+// a short tile costs both the same.
+template <int FORM, int EPI, int W, int BM, int U, int BK, int NSA, int NSB>
 __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, uint8_t* smem) {
-    constexpr int kRowBytes = BM * kBK * 2, kColRing = NSA * kRowBytes;
-    constexpr int kADma = kRowBytes / 1024 / kWaves, kBDma = kColBytes / 1024 / kWaves;
+    constexpr int WM = W / 4;
+    constexpr int kRowBytes = BM * BK * 2, kColStage = kBN * BK * 2, kColRing = NSA * kRowBytes;
+    constexpr int kADma = kRowBytes / 1024 / W, kBDma = kColStage / 1024 / W;
+    constexpr int kDmaRows = 512 / BK, kUnits = BK / 8;       // rows of a DMA, 16-byte units of a row (RC)
     constexpr bool kGateUp = FORM == kNT && EPI == kSwiglu;   // 128 gate + 128 up columns per tile
     constexpr int kTileCols = kGateUp ? kBN / 2 : kBN;        // output columns per tile
     const int lane = threadIdx.x & 63;
@@ -298,8 +304,8 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
     const int64_t abase = P.slots ? 0 : (int64_t)t.p0 * P.R;
 #pragma unroll
     for (int i = 0; i < kADma; ++i) {
-        const int r = (i * kWaves + wave) * 8 + (lane >> 3);
-        aunit[i] = (lane & 7) ^ ((r >> 1) & 7);
+        const int r = (i * W + wave) * kDmaRows + lane / kUnits;
+        aunit[i] = (lane % kUnits) ^ rc_swizzle<BK>(r);
         int src = r;
         bool ok = r < t.rows;
         if (P.slots && ok) {
@@ -316,52 +322,52 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
 #pragma unroll
     for (int i = 0; i < kBDma; ++i) {
         if constexpr (FORM == kNT) {
-            const int r = (i * kWaves + wave) * 8 + (lane >> 3);
+            const int r = (i * W + wave) * kDmaRows + lane / kUnits;
             const int n = kGateUp ? r & (kBN / 2 - 1) : r;
-            bpos[i] = (lane & 7) ^ ((r >> 1) & 7);
+            bpos[i] = (lane % kUnits) ^ rc_swizzle<BK>(r);
             boff[i] = c0 + n < P.C ? (uint32_t)n * (uint32_t)P.R * 2u + bpos[i] * 16 : kOutside;
         } else {
-            const int r = (i * kWaves + wave) * 2 + (lane >> 5);
+            const int r = (i * W + wave) * 2 + (lane >> 5);
             const int pos = lane & 31, col = (((pos >> 1) ^ ro_swizzle(r)) << 4) + ((pos & 1) << 3);
             bpos[i] = r;
             boff[i] = c0 + col < P.C ? (uint32_t)r * (uint32_t)P.C * 2u + col * 2 : kOutside;
         }
     }
 
-    const int spp = (P.R + kBK - 1) / kBK;          // stages per pair
+    const int spp = (P.R + BK - 1) / BK;            // stages per pair
     const int nstages = spp * P.pairs;
     const auto dma_a = [&](int s) {
         const int pair = FORM == kNN && s >= spp ? 1 : 0;
-        const int r0 = (s - pair * spp) * kBK;
+        const int r0 = (s - pair * spp) * BK;
         const uint16_t* a = uniform_ptr((pair ? P.a1 : P.a0) + abase + r0);
         const uint32_t buf = lds0 + (s % NSA) * kRowBytes;
 #pragma unroll
         for (int i = 0; i < kADma; ++i) {
             const uint32_t vo = r0 + aunit[i] * 8 < P.R ? aoff[i] : kOutside;
-            lds_dma16_buf(a, vo, buf + (i * kWaves + wave) * 1024);
+            lds_dma16_buf(a, vo, buf + (i * W + wave) * 1024);
         }
     };
     const auto dma_b = [&](int s) {
         const int pair = FORM == kNN && s >= spp ? 1 : 0;
-        const int r0 = (s - pair * spp) * kBK;
-        const uint32_t buf = lds0 + kColRing + (s % NSB) * kColBytes;
+        const int r0 = (s - pair * spp) * BK;
+        const uint32_t buf = lds0 + kColRing + (s % NSB) * kColStage;
 #pragma unroll
         for (int i = 0; i < kBDma; ++i) {
             const bool up = kGateUp && i >= kBDma / 2;
             const uint16_t* w = uniform_ptr((pair || up ? P.w1 : P.w0) + wbase + (FORM == kNT ? (int64_t)r0 : (int64_t)r0 * P.C));
             const bool ok = FORM == kNT ? r0 + bpos[i] * 8 < P.R : r0 + bpos[i] < P.R;
-            lds_dma16_buf(w, ok ? boff[i] : kOutside, buf + (i * kWaves + wave) * 1024);
+            lds_dma16_buf(w, ok ? boff[i] : kOutside, buf + (i * W + wave) * 1024);
         }
     };
 
     // lane offsets of the fragments
-    int aread[2], bread[2], bchunk[kNI];
+    int aread[BK / 32], bread[BK / 32], bchunk[kNI];
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-        const int u = ((ks * 4 + q) ^ (lrow >> 1)) * 16;
-        aread[ks] = (wm * 16 + lrow) * 128 + u;
+    for (int ks = 0; ks < BK / 32; ++ks) {
+        const int u = ((ks * 4 + q) ^ rc_swizzle<BK>(lrow)) * 16;
+        aread[ks] = (wm * 16 + lrow) * BK * 2 + u;
         if constexpr (FORM == kNT)
-            bread[ks] = ((kGateUp ? wn * 32 : wn * 64) + lrow) * 128 + u;
+            bread[ks] = ((kGateUp ? wn * 32 : wn * 64) + lrow) * BK * 2 + u;
         else
             bread[ks] = (ks * 32 + q * 8 + (lrow >> 2)) * 512 + (lrow & 3) * 8;
     }
@@ -374,22 +380,28 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
     for (int mi = 0; mi < U; ++mi)
 #pragma unroll
         for (int ni = 0; ni < kNI; ++ni) acc[mi][ni] = floatx4{0, 0, 0, 0};
-    run_stages<NSA, NSB, U, kNI, kADma, kBDma, 1, FORM == kNT ? 1 : 2>(
-        nstages, dma_a, dma_b,
-        [&](int buf, int ks, int mi) { return frag_rc((const lds_u8*)smem + buf * kRowBytes, aread[ks], 2 * mi); },
-        [&](int buf, int ks, int ni) {
-            const lds_u8* bs = (const lds_u8*)smem + kColRing + buf * kColBytes;
-            if constexpr (FORM == kNT) return frag_rc(bs, bread[ks], kGateUp && ni >= 2 ? ni + 6 : ni);
-            else return frag_ro<512>(bs, bread[ks] + bchunk[ni]);
-        },
-        acc);
+    const auto read_a = [&](int buf, int ks, int mi) {
+        return frag_rc<BK>((const lds_u8*)smem + buf * kRowBytes, aread[ks], WM * mi);
+    };
+    const auto read_b = [&](int buf, int ks, int ni) {
+        const lds_u8* bs = (const lds_u8*)smem + kColRing + buf * kColStage;
+        if constexpr (FORM == kNT) return frag_rc<BK>(bs, bread[ks], kGateUp && ni >= 2 ? ni + 6 : ni);
+        else return frag_ro<512>(bs, bread[ks] + bchunk[ni]);
+    };
+    constexpr int kReadsB = FORM == kNT ? 1 : 2;
+    if constexpr (BK == 64)
+        run_stages<NSA, NSB, U, kNI, kADma, kBDma, 1, kReadsB>(nstages, dma_a, dma_b, read_a, read_b, acc);
+    else
+        run_steps<NSA, U, kNI, kADma + kBDma, 1, kReadsB>(
+            nstages, [&](int s) { dma_a(s); dma_b(s); }, [&](int buf, int mi) { return read_a(buf, 0, mi); },
+            [&](int buf, int ni) { return read_b(buf, 0, ni); }, acc);
 
     // One rounding to bf16 per output; a lane stores eight columns of one row.
     // Every lane takes part in the exchanges, also those that store nothing.
     constexpr int kPairs = kGateUp ? 1 : 2;
 #pragma unroll
     for (int mi = 0; mi < U; ++mi) {
-        const int r = mi * 32 + wm * 16 + lrow;
+        const int r = (mi * WM + wm) * 16 + lrow;
         const int64_t row = (int64_t)(t.p0 + r) * P.C;
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
@@ -412,11 +424,10 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
                 }
             } else if constexpr (EPI == kSwiglu) {
                 // dh = acc; da = dh b s (1 + a (1 - s)), db = dh a s, s = sigmoid(a)
-                uint4 av = make_uint4(0, 0, 0, 0), bv = av;
-                if (ok) {
-                    av = *reinterpret_cast<const uint4*>(P.i0 + row + c);
-                    bv = *reinterpret_cast<const uint4*>(P.i1 + row + c);
-                }
+                // lanes outside read the tile's last row or columns, so that no
+                // load waits behind a branch
+                const int64_t at = (int64_t)(t.p0 + min(r, t.rows - 1)) * P.C + min(c, P.C - 8);
+                uint4 av = *reinterpret_cast<const uint4*>(P.i0 + at), bv = *reinterpret_cast<const uint4*>(P.i1 + at);
                 const Pair4 ap = exchange_back(av), bp = exchange_back(bv);
                 const floatx4 a[2] = {widen4(ap.a0, ap.a1), widen4(ap.b0, ap.b1)};
                 const floatx4 b[2] = {widen4(bp.a0, bp.a1), widen4(bp.b0, bp.b1)};
@@ -453,15 +464,30 @@ __global__ void __launch_bounds__(kThreads, BM == 64 ? 4 : 2) k_rows_mm(MmParams
     constexpr int N64 = BM == 64 ? 2 : 4;
     const RowTile t = find_tile<BM>(P, blockIdx.x);
     if (t.e < 0) return;
-    if (t.rows <= 32) rows_tile<FORM, EPI, 64, 1, N64, N64>(P, t, smem);
-    else if (BM == 64 || t.rows <= 64) rows_tile<FORM, EPI, 64, 2, N64, N64>(P, t, smem);
+    if (t.rows <= 32) rows_tile<FORM, EPI, 8, 64, 1, 64, N64, N64>(P, t, smem);
+    else if (BM == 64 || t.rows <= 64) rows_tile<FORM, EPI, 8, 64, 2, 64, N64, N64>(P, t, smem);
     else if constexpr (BM > 64) {
-        if (t.rows <= 96) rows_tile<FORM, EPI, 128, 3, 3, 3>(P, t, smem);
-        else if (t.rows <= 128) rows_tile<FORM, EPI, 128, 4, 3, 3>(P, t, smem);
-        else if (t.rows <= 160) rows_tile<FORM, EPI, 192, 5, 2, 3>(P, t, smem);
-        else if (t.rows <= 192) rows_tile<FORM, EPI, 192, 6, 2, 3>(P, t, smem);
-        else rows_tile<FORM, EPI, 256, 8, 2, 3>(P, t, smem);
+        if (t.rows <= 96) rows_tile<FORM, EPI, 8, 128, 3, 64, 3, 3>(P, t, smem);
+        else if (t.rows <= 128) rows_tile<FORM, EPI, 8, 128, 4, 64, 3, 3>(P, t, smem);
+        else if (t.rows <= 160) rows_tile<FORM, EPI, 8, 192, 5, 64, 2, 3>(P, t, smem);
+        else if (t.rows <= 192) rows_tile<FORM, EPI, 8, 192, 6, 64, 2, 3>(P, t, smem);
+        else rows_tile<FORM, EPI, 8, 256, 8, 64, 2, 3>(P, t, smem);
     }
+}
+
+// Tiles of up to 128 rows on four waves, two workgroups a CU: one's first
+// loads and last stores run beside the other's products.
+template <int FORM, int EPI>
+__global__ void __launch_bounds__(kThreads / 2, 2) k_rows_mm4(MmParams P) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    const RowTile t = find_tile<128>(P, blockIdx.x);
+    if (t.e < 0) return;
+    if (t.rows <= 16) rows_tile<FORM, EPI, 4, 128, 1, 32, 3, 3>(P, t, smem);
+    else if (t.rows <= 32) rows_tile<FORM, EPI, 4, 128, 2, 32, 3, 3>(P, t, smem);
+    else if (t.rows <= 64) rows_tile<FORM, EPI, 4, 128, 4, 32, 3, 3>(P, t, smem);
+    else if (t.rows <= 80) rows_tile<FORM, EPI, 4, 128, 5, 32, 3, 3>(P, t, smem);
+    else if (t.rows <= 96) rows_tile<FORM, EPI, 4, 128, 6, 32, 3, 3>(P, t, smem);
+    else rows_tile<FORM, EPI, 4, 128, 8, 32, 3, 3>(P, t, smem);
 }
 
 // ---------------------------------------------------------------- weight gradient
@@ -658,8 +684,9 @@ int64_t row_tiles_bound(int M, int E, int BM) { return M / BM + (int64_t)std::mi
 template <int FORM, int EPI, int BM>
 moe_status launch_rows(const MmParams& P, const char* name, hipStream_t s) {
     const int64_t grid = xcd_grid(row_tiles_bound(P.M, P.E, BM) * P.ntc);
-    const size_t lds = BM == 64 ? rows_lds(64, 2, 2) : rows_lds(256, 2, 3);
-    static_assert(rows_lds(256, 2, 3) >= rows_lds(64, 4, 4) && rows_lds(256, 2, 3) >= rows_lds(128, 3, 3), "one size");
+    constexpr size_t lds = BM == 64 ? rows_lds(64, 64, 2, 2) : rows_lds(256, 64, 2, 3);
+    static_assert(rows_lds(256, 64, 2, 3) >= rows_lds(64, 64, 4, 4) && rows_lds(256, 64, 2, 3) >= rows_lds(128, 64, 3, 3),
+                  "one size");
     moe_status st = allow_dynamic_lds(reinterpret_cast<const void*>(&k_rows_mm<FORM, EPI, BM>), lds);
     if (st != MOE_OK) return st;
     MOE_LAUNCH(name, (k_rows_mm<FORM, EPI, BM>), dim3((unsigned)grid), dim3(kThreads), lds, s, P);
@@ -667,9 +694,20 @@ moe_status launch_rows(const MmParams& P, const char* name, hipStream_t s) {
 }
 
 template <int FORM, int EPI>
+moe_status launch_rows4(const MmParams& P, const char* name, hipStream_t s) {
+    const int64_t grid = xcd_grid(row_tiles_bound(P.M, P.E, 128) * P.ntc);
+    constexpr size_t lds = rows_lds(128, 32, 3, 3);
+    moe_status st = allow_dynamic_lds(reinterpret_cast<const void*>(&k_rows_mm4<FORM, EPI>), lds);
+    if (st != MOE_OK) return st;
+    MOE_LAUNCH(name, (k_rows_mm4<FORM, EPI>), dim3((unsigned)grid), dim3(kThreads / 2), lds, s, P);
+    return MOE_OK;
+}
+
+template <int FORM, int EPI>
 moe_status launch_rows_any(const MmParams& P, const char* name, hipStream_t s) {
     const int64_t mean = P.M / std::max(1, std::min(P.E, P.M));
     if (mean > 48) return launch_rows<FORM, EPI, 256>(P, name, s);
+    if (mean > 48) return launch_rows4<FORM, EPI>(P, name, s);
     return launch_rows<FORM, EPI, 64>(P, name, s);
 }
 
@@ -691,13 +729,12 @@ WgradPlan wgrad_plan(int M, int N, int K, int E) {
     p.ntn = (N + TM - 1) / TM;
     const int64_t per = (int64_t)p.ntn * p.ntk, slots = p.big ? 256 : 512;
     p.slice = 1 << 30;
-    // Few tiles: slices, so that their number comes near the workgroups that
-    // run at once.  Not under 16 stages with several experts (the join and its
-    // partial sums cost as much as 10 to 20 stages, and only a long expert is
-    // then cut at all), 8 with one, whose rows are known.
+    // Few tiles: slices of at least 8 stages (the join and its partial sums
+    // cost as much), so that their number comes near the workgroups that run
+    // at once.
     if (2 * per * E <= slots) {
         const int64_t want = slots / per, stages = (M + kBK - 1) / kBK;
-        const int64_t rows = std::max<int64_t>((stages + want - 1) / want, E == 1 ? 8 : 16) * kBK;
+        const int64_t rows = std::max<int64_t>((stages + want - 1) / want, 8) * kBK;
         if (rows < M) p.slice = (int)rows;
     }
     p.parts = p.slice < M ? 2 * (M / p.slice) + 2 : 0;

@@ -105,6 +105,9 @@ def test_zero_tokens_and_no_rows():
     assert B.moe_combine(y, none, 4).shape == (0, 64)
     gone = torch.full((6,), -1, dtype=torch.int32, device=DEV)
     assert (B.moe_combine(torch.empty((1, 64), dtype=BF, device=DEV), gone, 3) == 0).all()
+    assert (B.moe_combine(y, gone, 3) == 0).all()          # no rows at all
     w = torch.full((2, 3), 1 / 3, device=DEV)
+    dy, dw = B.moe_combine_backward(torch.ones((2, 64), dtype=BF, device=DEV), y, gone, w)
+    assert dy.shape == (0, 64) and (dw == 0).all()
     dy, dw = B.moe_combine_backward(torch.ones((2, 64), dtype=BF, device=DEV), torch.ones((1, 64), dtype=BF, device=DEV), gone, w)
     assert dy.shape == (1, 64) and (dw == 0).all()
