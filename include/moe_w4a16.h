@@ -413,6 +413,11 @@ moe_status moe_w4a16_shared_expert(const uint16_t *d_x, int32_t T, int32_t H, in
  * The gradient of x itself (where rows were gathered) is moe_combine of dx's
  * rows without weights.
  *
+ * d_ws of the first four: moe_grouped_workspace_size(M, E, R, C, products)
+ * bytes, R the length of the sum (K forward, N in the gradients), C the
+ * columns of the result, products one of MOE_GROUPED_*.  It is 0, and d_ws may
+ * be NULL, but where a few rows meet a long sum; no initialisation.
+ *
  * N and K multiples of 8 and at most 2^20; E <= 1024; X * K * 2 < 2^32 - 256
  * where rows are gathered; fewer than 2^22 tiles: (M / 64 + E) * (max(N, K) /
  * 128), for the weight gradient also E * (N / 128) * (K / 128)
@@ -422,19 +427,25 @@ moe_status moe_w4a16_shared_expert(const uint16_t *d_x, int32_t T, int32_t H, in
  * There is no upper limit on d_offsets[E] - d_offsets[0] but M, and the host
  * never reads the offsets.
  */
+#define MOE_GROUPED_ONE    1   /* moe_grouped_linear; moe_grouped_linear_dgrad and moe_grouped_swiglu_dgrad */
+#define MOE_GROUPED_PAIR   2   /* moe_grouped_linear_dgrad with d_dy2 */
+#define MOE_GROUPED_SWIGLU 3   /* moe_grouped_swiglu */
+size_t moe_grouped_workspace_size(int32_t M, int32_t E, int32_t R, int32_t C, int32_t products);
 moe_status moe_grouped_linear(const uint16_t *d_x, int32_t X, int32_t K, const uint16_t *d_w, int32_t E, int32_t N,
                               const int32_t *d_offsets, const int32_t *d_sorted_slots, int32_t k, int32_t M,
-                              uint16_t *d_y, hipStream_t stream);
+                              uint16_t *d_y, void *d_ws, size_t ws_bytes, hipStream_t stream);
 moe_status moe_grouped_swiglu(const uint16_t *d_x, int32_t X, int32_t K, const uint16_t *d_gate,
                               const uint16_t *d_up, int32_t E, int32_t N, const int32_t *d_offsets,
                               const int32_t *d_sorted_slots, int32_t k, int32_t M, uint16_t *d_h, uint16_t *d_a,
-                              uint16_t *d_b, hipStream_t stream);
+                              uint16_t *d_b, void *d_ws, size_t ws_bytes, hipStream_t stream);
 moe_status moe_grouped_linear_dgrad(const uint16_t *d_dy, const uint16_t *d_w, const uint16_t *d_dy2,
                                     const uint16_t *d_w2, int32_t M, int32_t N, int32_t E, int32_t K,
-                                    const int32_t *d_offsets, uint16_t *d_dx, hipStream_t stream);
+                                    const int32_t *d_offsets, uint16_t *d_dx, void *d_ws, size_t ws_bytes,
+                                    hipStream_t stream);
 moe_status moe_grouped_swiglu_dgrad(const uint16_t *d_dy, const uint16_t *d_w, int32_t M, int32_t N, int32_t E,
                                     int32_t K, const int32_t *d_offsets, const uint16_t *d_a, const uint16_t *d_b,
-                                    uint16_t *d_da, uint16_t *d_db, hipStream_t stream);
+                                    uint16_t *d_da, uint16_t *d_db, void *d_ws, size_t ws_bytes,
+                                    hipStream_t stream);
 size_t moe_grouped_linear_wgrad_workspace_size(int32_t M, int32_t N, int32_t K, int32_t E);
 moe_status moe_grouped_linear_wgrad(const uint16_t *d_dy, int32_t M, int32_t N, const uint16_t *d_x, int32_t X,
                                     int32_t K, int32_t E, const int32_t *d_offsets, const int32_t *d_sorted_slots,

@@ -78,10 +78,11 @@ _SIGS = {
                                              _P]),
     "moe_router_route_workspace_size": (_S, [_I, _I, _I]),
     "moe_router_route_topk": (_I, [_P, _I, _I, _P, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P]),
-    "moe_grouped_linear": (_I, [_P, _I, _I, _P, _I, _I, _P, _P, _I, _I, _P, _P]),
-    "moe_grouped_swiglu": (_I, [_P, _I, _I, _P, _P, _I, _I, _P, _P, _I, _I, _P, _P, _P, _P]),
-    "moe_grouped_linear_dgrad": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P]),
-    "moe_grouped_swiglu_dgrad": (_I, [_P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "moe_grouped_workspace_size": (_S, [_I, _I, _I, _I, _I]),
+    "moe_grouped_linear": (_I, [_P, _I, _I, _P, _I, _I, _P, _P, _I, _I, _P, _P, _S, _P]),
+    "moe_grouped_swiglu": (_I, [_P, _I, _I, _P, _P, _I, _I, _P, _P, _I, _I, _P, _P, _P, _P, _S, _P]),
+    "moe_grouped_linear_dgrad": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _S, _P]),
+    "moe_grouped_swiglu_dgrad": (_I, [_P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _S, _P]),
     "moe_grouped_linear_wgrad_workspace_size": (_S, [_I, _I, _I, _I]),
     "moe_grouped_linear_wgrad": (_I, [_P, _I, _I, _P, _I, _I, _I, _P, _P, _I, _I, _P, _P, _S, _P]),
     "moe_int4_quantize_pack": (_I, [_P, _IP, _P]),
@@ -612,22 +613,46 @@ def _rows(x, sorted_slots):
     return M, _same(sorted_slots, "sorted_slots", x, _I32, (M,))
 
 
+GROUPED_ONE, GROUPED_PAIR, GROUPED_SWIGLU = 1, 2, 3
+
+
+def moe_grouped_workspace_size(M, E, R, C, products=GROUPED_ONE):
+    return int(lib().moe_grouped_workspace_size(M, E, R, C, products))
+
+
+def _workspace(ws, need, like):
+    """(address, bytes) of a workspace of at least `need` bytes on `like`'s
+    device (allocated if None), and the tensor, to be kept until the launch."""
+    if ws is None:
+        if need == 0:
+            return None, 0, None
+        ws = like.new_empty((need,), dtype=torch.uint8)
+    _dev_tensor(ws, "ws", min_bytes=need)
+    return _same(ws, "ws", like, (ws.dtype,), ws.shape), ws.numel() * ws.element_size(), ws
+
+
 @_entry
-def moe_grouped_linear(x, w, offsets, sorted_slots=None, k=1, out=None):
+def moe_grouped_linear(x, w, offsets, sorted_slots=None, k=1, out=None, ws=None):
     """y = x . W^T by expert: x bf16 [X, K] (values or bits), w [E, N, K],
     offsets int32 [E + 1]; with sorted_slots (int32 [M]) row p of the result
-    reads x's row sorted_slots[p] // k.  Returns [M, N] in x's dtype."""
+    reads x's row sorted_slots[p] // k.  Returns [M, N] in x's dtype.  ws (here
+    and below): a workspace of moe_grouped_workspace_size bytes, allocated if
+    None."""
     (X, K), (E, N, _) = _dims(x, "x", 2), _dims(w, "w", 3)
     px, pw = _same(x, "x", x, _BITS16, (X, K)), _same(w, "w", x, _BITS16, (E, N, K))
     po = _same(offsets, "offsets", x, _I32, (E + 1,))
     M, ps = _rows(x, sorted_slots)
     out = _new(out, "out", x, x.dtype, (M, N))
-    _check(lib().moe_grouped_linear(px, X, K, pw, E, N, po, ps, k, M, out.data_ptr(), _here(x)), "moe_grouped_linear")
+    L = lib()
+    pws, nws, ws = _workspace(ws, L.moe_grouped_workspace_size(M, E, K, N, GROUPED_ONE), x)
+    _check(L.moe_grouped_linear(px, X, K, pw, E, N, po, ps, k, M, out.data_ptr(), pws, nws, _here(x)),
+           "moe_grouped_linear")
     return out
 
 
 @_entry
-def moe_grouped_swiglu(x, gate, up, offsets, sorted_slots=None, k=1, h=None, a=None, b=None, save=False):
+def moe_grouped_swiglu(x, gate, up, offsets, sorted_slots=None, k=1, h=None, a=None, b=None, save=False,
+                       ws=None):
     """h = silu(x . gate^T) * (x . up^T) by expert, rows as in
     moe_grouped_linear.  Returns h, or (h, a, b) with save (or with a and b
     given): the two products, for moe_grouped_swiglu_dgrad."""
@@ -640,13 +665,15 @@ def moe_grouped_swiglu(x, gate, up, offsets, sorted_slots=None, k=1, h=None, a=N
     h = _new(h, "h", x, x.dtype, (M, N))
     if save:
         a, b = _new(a, "a", x, x.dtype, (M, N)), _new(b, "b", x, x.dtype, (M, N))
-    _check(lib().moe_grouped_swiglu(px, X, K, pg, pu, E, N, po, ps, k, M, h.data_ptr(), a.data_ptr() if save else None,
-                                    b.data_ptr() if save else None, _here(x)), "moe_grouped_swiglu")
+    L = lib()
+    pws, nws, ws = _workspace(ws, L.moe_grouped_workspace_size(M, E, K, N, GROUPED_SWIGLU), x)
+    _check(L.moe_grouped_swiglu(px, X, K, pg, pu, E, N, po, ps, k, M, h.data_ptr(), a.data_ptr() if save else None,
+                                b.data_ptr() if save else None, pws, nws, _here(x)), "moe_grouped_swiglu")
     return (h, a, b) if save else h
 
 
 @_entry
-def moe_grouped_linear_dgrad(dy, w, offsets, dy2=None, w2=None, out=None):
+def moe_grouped_linear_dgrad(dy, w, offsets, dy2=None, w2=None, out=None, ws=None):
     """dx = dy . W (+ dy2 . W2) by expert: dy [M, N], w [E, N, K] -> [M, K]
     in dy's dtype."""
     (M, N), (E, _, K) = _dims(dy, "dy", 2), _dims(w, "w", 3)
@@ -658,13 +685,16 @@ def moe_grouped_linear_dgrad(dy, w, offsets, dy2=None, w2=None, out=None):
     if dy2 is not None:
         pd2, pw2 = _same(dy2, "dy2", dy, _BITS16, (M, N)), _same(w2, "w2", dy, _BITS16, (E, N, K))
     out = _new(out, "out", dy, dy.dtype, (M, K))
-    _check(lib().moe_grouped_linear_dgrad(pd, pw, pd2, pw2, M, N, E, K, po, out.data_ptr(), _here(dy)),
+    L = lib()
+    pws, nws, ws = _workspace(ws, L.moe_grouped_workspace_size(M, E, N, K, GROUPED_ONE if dy2 is None else GROUPED_PAIR),
+                              dy)
+    _check(L.moe_grouped_linear_dgrad(pd, pw, pd2, pw2, M, N, E, K, po, out.data_ptr(), pws, nws, _here(dy)),
            "moe_grouped_linear_dgrad")
     return out
 
 
 @_entry
-def moe_grouped_swiglu_dgrad(dy, w, a, b, offsets, da=None, db=None):
+def moe_grouped_swiglu_dgrad(dy, w, a, b, offsets, da=None, db=None, ws=None):
     """(da, db): the gradient through the down projection w [E, N, K] and
     SwiGLU, with a and b [M, K] as moe_grouped_swiglu saved them."""
     (M, N), (E, _, K) = _dims(dy, "dy", 2), _dims(w, "w", 3)
@@ -672,7 +702,9 @@ def moe_grouped_swiglu_dgrad(dy, w, a, b, offsets, da=None, db=None):
     pa, pb = _same(a, "a", dy, _BITS16, (M, K)), _same(b, "b", dy, _BITS16, (M, K))
     po = _same(offsets, "offsets", dy, _I32, (E + 1,))
     da, db = _new(da, "da", dy, dy.dtype, (M, K)), _new(db, "db", dy, dy.dtype, (M, K))
-    _check(lib().moe_grouped_swiglu_dgrad(pd, pw, M, N, E, K, po, pa, pb, da.data_ptr(), db.data_ptr(), _here(dy)),
+    L = lib()
+    pws, nws, ws = _workspace(ws, L.moe_grouped_workspace_size(M, E, N, K, GROUPED_ONE), dy)
+    _check(L.moe_grouped_swiglu_dgrad(pd, pw, M, N, E, K, po, pa, pb, da.data_ptr(), db.data_ptr(), pws, nws, _here(dy)),
            "moe_grouped_swiglu_dgrad")
     return da, db
 
@@ -693,16 +725,9 @@ def moe_grouped_linear_wgrad(dy, x, offsets, sorted_slots=None, k=1, out=None, a
         raise ValueError("accumulate needs out")
     out = _new(out, "out", dy, torch.float32, (E, N, K))
     L = lib()
-    need = L.moe_grouped_linear_wgrad_workspace_size(M, N, K, E)
-    if ws is None and need:
-        ws = torch.empty((need,), dtype=torch.uint8, device=dy.device)
-    if ws is not None:
-        _dev_tensor(ws, "ws", min_bytes=need)
-        _same(ws, "ws", dy, (ws.dtype,), ws.shape)
-    _check(L.moe_grouped_linear_wgrad(pd, M, N, px, X, K, E, po, ps, k, int(bool(accumulate)), out.data_ptr(),
-                                      None if ws is None else ws.data_ptr(),
-                                      0 if ws is None else ws.numel() * ws.element_size(), _here(dy)),
-           "moe_grouped_linear_wgrad")
+    pws, nws, ws = _workspace(ws, L.moe_grouped_linear_wgrad_workspace_size(M, N, K, E), dy)
+    _check(L.moe_grouped_linear_wgrad(pd, M, N, px, X, K, E, po, ps, k, int(bool(accumulate)), out.data_ptr(), pws, nws,
+                                      _here(dy)), "moe_grouped_linear_wgrad")
     return out
 
 

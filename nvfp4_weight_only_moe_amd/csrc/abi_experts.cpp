@@ -53,6 +53,13 @@ moe_status check_group_shape(int32_t M, int32_t N, int32_t K, int32_t E) {
     return MOE_OK;
 }
 
+// A workspace of `need` bytes, apart from the call's buffers.
+moe_status check_ws(void* d_ws, size_t ws_bytes, size_t need, std::initializer_list<Buf> bufs) {
+    if (need == 0) return MOE_OK;
+    if (!d_ws || ws_bytes < need) return MOE_ERR_WORKSPACE;
+    return check_apart({Buf{d_ws, need}}, bufs);
+}
+
 // x's rows: gathered through sorted slots (slot / k), or row p for row p.
 moe_status check_rows(int32_t X, int32_t M, int32_t K, const int32_t* slots, int32_t k) {
     if (X < 0) return MOE_ERR_SHAPE;
@@ -82,9 +89,14 @@ size_t int4_groups(const moe_int4_tensor* t) { return (size_t)t->E * t->N * (t->
 
 extern "C" {
 
+size_t moe_grouped_workspace_size(int32_t M, int32_t E, int32_t R, int32_t C, int32_t products) {
+    if (products < 1 || products > 3 || check_group_shape(M, C, R, E) != MOE_OK || M == 0) return 0;
+    return grouped_rows_workspace_bytes(M, E, R, C, products == MOE_GROUPED_PAIR ? 2 : 1, products == MOE_GROUPED_SWIGLU);
+}
+
 moe_status moe_grouped_linear(const uint16_t* d_x, int32_t X, int32_t K, const uint16_t* d_w, int32_t E, int32_t N,
                               const int32_t* d_offsets, const int32_t* d_sorted_slots, int32_t k, int32_t M,
-                              uint16_t* d_y, hipStream_t stream) {
+                              uint16_t* d_y, void* d_ws, size_t ws_bytes, hipStream_t stream) {
     moe_status st = check_group_shape(M, N, K, E);
     if (st != MOE_OK) return st;
     if (M == 0) return MOE_OK;
@@ -93,17 +105,19 @@ moe_status moe_grouped_linear(const uint16_t* d_x, int32_t X, int32_t K, const u
         slots{d_sorted_slots, (size_t)M * 4}, y{d_y, b16(M, N)};
     if ((st = check_present({x, w, off, y})) != MOE_OK) return st;
     if ((st = check_apart({y}, {x, w, off, slots})) != MOE_OK) return st;
+    if ((st = check_ws(d_ws, ws_bytes, grouped_rows_workspace_bytes(M, E, K, N, 1, false), {x, w, off, slots, y})) != MOE_OK)
+        return st;
     GroupedArgs g{};
     g.x = d_x; g.w = d_w; g.offsets = d_offsets; g.slots = d_sorted_slots;
     g.E = E; g.M = M; g.X = X; g.k = d_sorted_slots ? k : 1; g.N = N; g.K = K;
     g.o0 = d_y;
-    return launch_grouped_fwd(g, stream);
+    return launch_grouped_fwd(g, d_ws, stream);
 }
 
 moe_status moe_grouped_swiglu(const uint16_t* d_x, int32_t X, int32_t K, const uint16_t* d_gate,
                               const uint16_t* d_up, int32_t E, int32_t N, const int32_t* d_offsets,
                               const int32_t* d_sorted_slots, int32_t k, int32_t M, uint16_t* d_h, uint16_t* d_a,
-                              uint16_t* d_b, hipStream_t stream) {
+                              uint16_t* d_b, void* d_ws, size_t ws_bytes, hipStream_t stream) {
     moe_status st = check_group_shape(M, N, K, E);
     if (st != MOE_OK) return st;
     if (M == 0) return MOE_OK;
@@ -114,16 +128,20 @@ moe_status moe_grouped_swiglu(const uint16_t* d_x, int32_t X, int32_t K, const u
         a{d_a, b16(M, N)}, b{d_b, b16(M, N)};
     if ((st = check_present({x, gate, up, off, h})) != MOE_OK) return st;
     if ((st = check_apart({h, a, b}, {x, gate, up, off, slots})) != MOE_OK) return st;
+    if ((st = check_ws(d_ws, ws_bytes, grouped_rows_workspace_bytes(M, E, K, N, 1, true),
+                       {x, gate, up, off, slots, h, a, b})) != MOE_OK)
+        return st;
     GroupedArgs g{};
     g.x = d_x; g.w = d_gate; g.w2 = d_up; g.offsets = d_offsets; g.slots = d_sorted_slots;
     g.E = E; g.M = M; g.X = X; g.k = d_sorted_slots ? k : 1; g.N = N; g.K = K;
     g.o0 = d_h; g.o1 = d_a; g.o2 = d_b;
-    return launch_grouped_fwd(g, stream);
+    return launch_grouped_fwd(g, d_ws, stream);
 }
 
 moe_status moe_grouped_linear_dgrad(const uint16_t* d_dy, const uint16_t* d_w, const uint16_t* d_dy2,
                                     const uint16_t* d_w2, int32_t M, int32_t N, int32_t E, int32_t K,
-                                    const int32_t* d_offsets, uint16_t* d_dx, hipStream_t stream) {
+                                    const int32_t* d_offsets, uint16_t* d_dx, void* d_ws, size_t ws_bytes,
+                                    hipStream_t stream) {
     moe_status st = check_group_shape(M, N, K, E);
     if (st != MOE_OK) return st;
     if (M == 0) return MOE_OK;
@@ -133,16 +151,20 @@ moe_status moe_grouped_linear_dgrad(const uint16_t* d_dy, const uint16_t* d_w, c
     if ((st = check_present({dy, w, off, dx})) != MOE_OK) return st;
     if (!aligned16(d_dy2) || !aligned16(d_w2)) return MOE_ERR_ALIGN;
     if ((st = check_apart({dx}, {dy, w, dy2, w2, off})) != MOE_OK) return st;
+    if ((st = check_ws(d_ws, ws_bytes, grouped_rows_workspace_bytes(M, E, N, K, d_dy2 ? 2 : 1, false),
+                       {dy, w, dy2, w2, off, dx})) != MOE_OK)
+        return st;
     GroupedArgs g{};
     g.dy = d_dy; g.dy2 = d_dy2; g.w = d_w; g.w2 = d_w2; g.offsets = d_offsets;
     g.E = E; g.M = M; g.N = N; g.K = K;
     g.o0 = d_dx;
-    return launch_grouped_dgrad(g, stream);
+    return launch_grouped_dgrad(g, d_ws, stream);
 }
 
 moe_status moe_grouped_swiglu_dgrad(const uint16_t* d_dy, const uint16_t* d_w, int32_t M, int32_t N, int32_t E,
                                     int32_t K, const int32_t* d_offsets, const uint16_t* d_a, const uint16_t* d_b,
-                                    uint16_t* d_da, uint16_t* d_db, hipStream_t stream) {
+                                    uint16_t* d_da, uint16_t* d_db, void* d_ws, size_t ws_bytes,
+                                    hipStream_t stream) {
     moe_status st = check_group_shape(M, N, K, E);
     if (st != MOE_OK) return st;
     if (M == 0) return MOE_OK;
@@ -150,11 +172,14 @@ moe_status moe_grouped_swiglu_dgrad(const uint16_t* d_dy, const uint16_t* d_w, i
         a{d_a, b16(M, K)}, b{d_b, b16(M, K)}, da{d_da, b16(M, K)}, db{d_db, b16(M, K)};
     if ((st = check_present({dy, w, off, a, b, da, db})) != MOE_OK) return st;
     if ((st = check_apart({da, db}, {dy, w, off, a, b})) != MOE_OK) return st;
+    if ((st = check_ws(d_ws, ws_bytes, grouped_rows_workspace_bytes(M, E, N, K, 1, false),
+                       {dy, w, off, a, b, da, db})) != MOE_OK)
+        return st;
     GroupedArgs g{};
     g.dy = d_dy; g.w = d_w; g.offsets = d_offsets;
     g.E = E; g.M = M; g.N = N; g.K = K;
     g.a = d_a; g.b = d_b; g.o0 = d_da; g.o1 = d_db;
-    return launch_grouped_dgrad(g, stream);
+    return launch_grouped_dgrad(g, d_ws, stream);
 }
 
 size_t moe_grouped_linear_wgrad_workspace_size(int32_t M, int32_t N, int32_t K, int32_t E) {
@@ -177,11 +202,8 @@ moe_status moe_grouped_linear_wgrad(const uint16_t* d_dy, int32_t M, int32_t N, 
         if ((st = check_rows(X, M, K, d_sorted_slots, k)) != MOE_OK) return st;
         if ((st = check_present({dy, x})) != MOE_OK) return st;
         if ((st = check_apart({dw}, {dy, x, off, slots})) != MOE_OK) return st;
-        const size_t need = grouped_wgrad_workspace_bytes(M, N, K, E);
-        if (need) {
-            if (!d_ws || ws_bytes < need) return MOE_ERR_WORKSPACE;
-            if ((st = check_apart({Buf{d_ws, need}}, {dy, x, off, slots, dw})) != MOE_OK) return st;
-        }
+        if ((st = check_ws(d_ws, ws_bytes, grouped_wgrad_workspace_bytes(M, N, K, E), {dy, x, off, slots, dw})) != MOE_OK)
+            return st;
     }
     GroupedArgs g{};
     g.dy = d_dy; g.x = d_x; g.offsets = d_offsets; g.slots = M > 0 ? d_sorted_slots : nullptr;

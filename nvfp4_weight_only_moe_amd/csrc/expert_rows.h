@@ -36,7 +36,7 @@ inline int64_t xcd_grid(int64_t total) { return total + 8 * ((total + 255) / 256
 // [0, M], so no piece leaves the buffers.
 // TALL: experts whose pieces, cut to equal heights, are taller than that come
 // first.  Workgroups start in order, so short ones then fill the last round
-// (32 experts of about 255 rows, 6 column tiles: 240 -> FIG us).
+// (32 experts of about 255 rows, 6 column tiles: 240 -> 218 us).
 struct Piece {
     int e, lo, n, pieces, idx, cut_before;
 };

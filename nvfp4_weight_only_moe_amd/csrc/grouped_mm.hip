@@ -40,8 +40,10 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
-enum Form { kNT = 0, kNN = 1 };
-enum Epilogue { kPlain = 0, kSwiglu = 1 };
+// x . W^T | x . gate^T and x . up^T | dy . W
+enum Form { kNT = 0, kGateUp = 1, kNN = 2 };
+// rounded outputs | SwiGLU, or its gradient (kNN) | fp32 sums of one slice of the reduction
+enum Epilogue { kPlain = 0, kSwiglu = 1, kPart = 2 };
 
 // 16 bytes per lane from (base + voff) to LDS at ldst + 16 * lane; lanes whose
 // voff lies outside the descriptor write zeros.  Inline assembly for the same
@@ -197,35 +199,39 @@ struct MmParams {
     uint16_t *o0, *o1, *o2;       // y | h, a, b | dx | da, db
     const uint16_t *i0, *i1;      // kSwiglu on NN: the saved a, b
     int ntc;                      // column tiles
+    int slices;                   // kPart: the reduction's slices
+    float* part;                  // kPart: [slices][1, gate/up: 2][M][C]
 };
 
 constexpr int kMGroup = 8;        // row tiles that run beside each other, sharing weight columns in L2
 
 struct RowTile {
     int e, p0, rows, ct;          // expert (-1: none), first row, rows of the tile, column tile
+    int slice;
 };
 
 // Tile of workgroup `bid`: inside an expert, kMGroup row tiles by all column
-// tiles after each other.
-template <int BM>
+// tiles after each other, each with its slices of the reduction.
+template <int BM, bool SLICED>
 __device__ __forceinline__ RowTile find_tile(const MmParams& P, int bid) {
-    const Piece f = find_piece<false, BM * 5 / 8>(P.offsets, P.E, P.M, BM, P.ntc, bid);
-    if (f.e < 0) return RowTile{-1, 0, 0, 0};
+    const Piece f = find_piece<false, BM * 5 / 8>(P.offsets, P.E, P.M, BM, SLICED ? P.ntc * P.slices : P.ntc, bid);
+    if (f.e < 0) return RowTile{-1, 0, 0, 0, 0};
+    const int idx = SLICED ? f.idx / P.slices : f.idx, slice = SLICED ? f.idx % P.slices : 0;
     const int full = f.pieces / kMGroup * kMGroup;
     int m, c;
-    if (f.idx < full * P.ntc) {
-        const int g = f.idx / (kMGroup * P.ntc), r = f.idx % (kMGroup * P.ntc);
+    if (idx < full * P.ntc) {
+        const int g = idx / (kMGroup * P.ntc), r = idx % (kMGroup * P.ntc);
         c = r / kMGroup;
         m = g * kMGroup + r % kMGroup;
     } else {
-        const int r = f.idx - full * P.ntc, last = f.pieces - full;
+        const int r = idx - full * P.ntc, last = f.pieces - full;
         c = r / last;
         m = full + r % last;
     }
     // equal heights, whole subtiles: tiles that share weight columns then move
     // through them in step and find each other's stages in L2
     const int h = ((f.n + f.pieces - 1) / f.pieces + 15) & ~15;
-    return RowTile{f.e, f.lo + m * h, min(h, f.n - m * h), c};
+    return RowTile{f.e, f.lo + m * h, min(h, f.n - m * h), c, slice};
 }
 
 // ---- fragments: lane l holds output position l & 15, reduction steps
@@ -251,6 +257,13 @@ __device__ __forceinline__ uint32_t pack_rne(float lo, float hi) {
 }
 // sigmoid with the reciprocal and exponential instructions (a few 2^-23 relative)
 __device__ __forceinline__ float sigmoid(float a) { return __builtin_amdgcn_rcpf(1.0f + __expf(-a)); }
+
+// dh through silu(a) b: da = dh b s (1 + a (1 - s)), db = dh a s, s = sigmoid(a)
+__device__ __forceinline__ void swiglu_grad(float dh, float a, float b, float& da, float& db) {
+    const float s = sigmoid(a), act = a * s;
+    db = dh * act;
+    da = dh * b * (s + act * (1.0f - s));
+}
 
 // A lane's four columns of two neighbouring 16-column subtiles <-> eight
 // columns of one of them: lane rows (16 lanes) 0 and 1 trade halves, and 2 and
@@ -289,8 +302,8 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
     constexpr int kRowBytes = BM * BK * 2, kColStage = kBN * BK * 2, kColRing = NSA * kRowBytes;
     constexpr int kADma = kRowBytes / 1024 / W, kBDma = kColStage / 1024 / W;
     constexpr int kDmaRows = 512 / BK, kUnits = BK / 8;       // rows of a DMA, 16-byte units of a row (RC)
-    constexpr bool kGateUp = FORM == kNT && EPI == kSwiglu;   // 128 gate + 128 up columns per tile
-    constexpr int kTileCols = kGateUp ? kBN / 2 : kBN;        // output columns per tile
+    constexpr bool RC = FORM != kNN, GU = FORM == kGateUp;    // GU: 128 gate + 128 up columns per tile
+    constexpr int kTileCols = GU ? kBN / 2 : kBN;             // output columns per tile
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave >> 2, wn = wave & 3;
@@ -318,12 +331,12 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
     // column operand
     uint32_t boff[kBDma];
     int bpos[kBDma];                                // RC: unit; RO: reduction row inside the stage
-    const int64_t wbase = FORM == kNT ? ((int64_t)t.e * P.C + c0) * P.R : (int64_t)t.e * P.R * P.C + c0;
+    const int64_t wbase = RC ? ((int64_t)t.e * P.C + c0) * P.R : (int64_t)t.e * P.R * P.C + c0;
 #pragma unroll
     for (int i = 0; i < kBDma; ++i) {
-        if constexpr (FORM == kNT) {
+        if constexpr (RC) {
             const int r = (i * W + wave) * kDmaRows + lane / kUnits;
-            const int n = kGateUp ? r & (kBN / 2 - 1) : r;
+            const int n = GU ? r & (kBN / 2 - 1) : r;
             bpos[i] = (lane % kUnits) ^ rc_swizzle<BK>(r);
             boff[i] = c0 + n < P.C ? (uint32_t)n * (uint32_t)P.R * 2u + bpos[i] * 16 : kOutside;
         } else {
@@ -335,10 +348,12 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
     }
 
     const int spp = (P.R + BK - 1) / BK;            // stages per pair
-    const int nstages = spp * P.pairs;
+    const int all = spp * P.pairs;
+    const int first = EPI == kPart ? (int)((int64_t)all * t.slice / P.slices) : 0;
+    const int nstages = (EPI == kPart ? (int)((int64_t)all * (t.slice + 1) / P.slices) : all) - first;
     const auto dma_a = [&](int s) {
-        const int pair = FORM == kNN && s >= spp ? 1 : 0;
-        const int r0 = (s - pair * spp) * BK;
+        const int pair = FORM == kNN && first + s >= spp ? 1 : 0;
+        const int r0 = (first + s - pair * spp) * BK;
         const uint16_t* a = uniform_ptr((pair ? P.a1 : P.a0) + abase + r0);
         const uint32_t buf = lds0 + (s % NSA) * kRowBytes;
 #pragma unroll
@@ -348,14 +363,14 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
         }
     };
     const auto dma_b = [&](int s) {
-        const int pair = FORM == kNN && s >= spp ? 1 : 0;
-        const int r0 = (s - pair * spp) * BK;
+        const int pair = FORM == kNN && first + s >= spp ? 1 : 0;
+        const int r0 = (first + s - pair * spp) * BK;
         const uint32_t buf = lds0 + kColRing + (s % NSB) * kColStage;
 #pragma unroll
         for (int i = 0; i < kBDma; ++i) {
-            const bool up = kGateUp && i >= kBDma / 2;
-            const uint16_t* w = uniform_ptr((pair || up ? P.w1 : P.w0) + wbase + (FORM == kNT ? (int64_t)r0 : (int64_t)r0 * P.C));
-            const bool ok = FORM == kNT ? r0 + bpos[i] * 8 < P.R : r0 + bpos[i] < P.R;
+            const bool up = GU && i >= kBDma / 2;
+            const uint16_t* w = uniform_ptr((pair || up ? P.w1 : P.w0) + wbase + (RC ? (int64_t)r0 : (int64_t)r0 * P.C));
+            const bool ok = RC ? r0 + bpos[i] * 8 < P.R : r0 + bpos[i] < P.R;
             lds_dma16_buf(w, ok ? boff[i] : kOutside, buf + (i * W + wave) * 1024);
         }
     };
@@ -366,8 +381,8 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
     for (int ks = 0; ks < BK / 32; ++ks) {
         const int u = ((ks * 4 + q) ^ rc_swizzle<BK>(lrow)) * 16;
         aread[ks] = (wm * 16 + lrow) * BK * 2 + u;
-        if constexpr (FORM == kNT)
-            bread[ks] = ((kGateUp ? wn * 32 : wn * 64) + lrow) * BK * 2 + u;
+        if constexpr (RC)
+            bread[ks] = ((GU ? wn * 32 : wn * 64) + lrow) * BK * 2 + u;
         else
             bread[ks] = (ks * 32 + q * 8 + (lrow >> 2)) * 512 + (lrow & 3) * 8;
     }
@@ -385,10 +400,10 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
     };
     const auto read_b = [&](int buf, int ks, int ni) {
         const lds_u8* bs = (const lds_u8*)smem + kColRing + buf * kColStage;
-        if constexpr (FORM == kNT) return frag_rc<BK>(bs, bread[ks], kGateUp && ni >= 2 ? ni + 6 : ni);
+        if constexpr (RC) return frag_rc<BK>(bs, bread[ks], GU && ni >= 2 ? ni + 6 : ni);
         else return frag_ro<512>(bs, bread[ks] + bchunk[ni]);
     };
-    constexpr int kReadsB = FORM == kNT ? 1 : 2;
+    constexpr int kReadsB = RC ? 1 : 2;
     if constexpr (BK == 64)
         run_stages<NSA, NSB, U, kNI, kADma, kBDma, 1, kReadsB>(nstages, dma_a, dma_b, read_a, read_b, acc);
     else
@@ -396,18 +411,33 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
             nstages, [&](int s) { dma_a(s); dma_b(s); }, [&](int buf, int mi) { return read_a(buf, 0, mi); },
             [&](int buf, int ni) { return read_b(buf, 0, ni); }, acc);
 
+    if constexpr (EPI == kPart) {
+#pragma unroll
+        for (int mi = 0; mi < U; ++mi) {
+            const int r = (mi * WM + wm) * 16 + lrow;
+            if (r >= t.rows) continue;
+#pragma unroll
+            for (int ni = 0; ni < kNI; ++ni) {
+                const int up = GU && ni >= 2 ? 1 : 0, c = c0 + (GU ? wn * 32 + ni % 2 * 16 : wn * 64 + ni * 16) + q * 4;
+                if (c >= P.C) continue;
+                const int64_t row = ((int64_t)(t.slice * (GU ? 2 : 1) + up) * P.M + t.p0 + r) * P.C;
+                *reinterpret_cast<floatx4*>(P.part + row + c) = acc[mi][ni];
+            }
+        }
+        return;
+    }
     // One rounding to bf16 per output; a lane stores eight columns of one row.
     // Every lane takes part in the exchanges, also those that store nothing.
-    constexpr int kPairs = kGateUp ? 1 : 2;
+    constexpr int kPairs = GU ? 1 : 2;
 #pragma unroll
     for (int mi = 0; mi < U; ++mi) {
         const int r = (mi * WM + wm) * 16 + lrow;
         const int64_t row = (int64_t)(t.p0 + r) * P.C;
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
-            const int c = c0 + (kGateUp ? wn * 32 : wn * 64 + j * 32) + (q & 1) * 16 + (q >> 1) * 8;
+            const int c = c0 + (GU ? wn * 32 : wn * 64 + j * 32) + (q & 1) * 16 + (q >> 1) * 8;
             const bool ok = r < t.rows && c < P.C;
-            if constexpr (kGateUp) {
+            if constexpr (GU) {
                 floatx4 h[2];
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
@@ -423,7 +453,6 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
                     }
                 }
             } else if constexpr (EPI == kSwiglu) {
-                // dh = acc; da = dh b s (1 + a (1 - s)), db = dh a s, s = sigmoid(a)
                 // lanes outside read the tile's last row or columns, so that no
                 // load waits behind a branch
                 const int64_t at = (int64_t)(t.p0 + min(r, t.rows - 1)) * P.C + min(c, P.C - 8);
@@ -436,9 +465,10 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float dh = acc[mi][2 * j + n][i], sg = sigmoid(a[n][i]), act = a[n][i] * sg;
-                        db[n][i] = dh * act;
-                        da[n][i] = dh * b[n][i] * (sg + act * (1.0f - sg));
+                        float x, y;                              // (elements of a vector bind to no reference)
+                        swiglu_grad(acc[mi][2 * j + n][i], a[n][i], b[n][i], x, y);
+                        da[n][i] = x;
+                        db[n][i] = y;
                     }
                 av = pack_pair(da[0], da[1]);
                 bv = pack_pair(db[0], db[1]);
@@ -457,12 +487,12 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
 // Tiles of up to BM rows, by their rows: a short tile waits for memory, not
 // for the matrix units, and its smaller stages leave room for more of them in
 // flight.  The weights, which come from HBM, have a stage more in flight than
-// the rows, which come from L2.  BM == 64: two workgroups a CU instead.
-template <int FORM, int EPI, int BM>
-__global__ void __launch_bounds__(kThreads, BM == 64 ? 4 : 2) k_rows_mm(MmParams P) {
+// the rows, which come from L2.  N64: stages of a 64-row tile in LDS, 4, or 2
+// for two workgroups a CU.
+template <int FORM, int EPI, int BM, int N64>
+__global__ void __launch_bounds__(kThreads, N64 == 2 ? 4 : 2) k_rows_mm(MmParams P) {
     extern __shared__ __align__(16) uint8_t smem[];
-    constexpr int N64 = BM == 64 ? 2 : 4;
-    const RowTile t = find_tile<BM>(P, blockIdx.x);
+    const RowTile t = find_tile<BM, EPI == kPart>(P, blockIdx.x);
     if (t.e < 0) return;
     if (t.rows <= 32) rows_tile<FORM, EPI, 8, 64, 1, 64, N64, N64>(P, t, smem);
     else if (BM == 64 || t.rows <= 64) rows_tile<FORM, EPI, 8, 64, 2, 64, N64, N64>(P, t, smem);
@@ -475,19 +505,53 @@ __global__ void __launch_bounds__(kThreads, BM == 64 ? 4 : 2) k_rows_mm(MmParams
     }
 }
 
-// Tiles of up to 128 rows on four waves, two workgroups a CU: one's first
-// loads and last stores run beside the other's products.
-template <int FORM, int EPI>
-__global__ void __launch_bounds__(kThreads / 2, 2) k_rows_mm4(MmParams P) {
-    extern __shared__ __align__(16) uint8_t smem[];
-    const RowTile t = find_tile<128>(P, blockIdx.x);
-    if (t.e < 0) return;
-    if (t.rows <= 16) rows_tile<FORM, EPI, 4, 128, 1, 32, 3, 3>(P, t, smem);
-    else if (t.rows <= 32) rows_tile<FORM, EPI, 4, 128, 2, 32, 3, 3>(P, t, smem);
-    else if (t.rows <= 64) rows_tile<FORM, EPI, 4, 128, 4, 32, 3, 3>(P, t, smem);
-    else if (t.rows <= 80) rows_tile<FORM, EPI, 4, 128, 5, 32, 3, 3>(P, t, smem);
-    else if (t.rows <= 96) rows_tile<FORM, EPI, 4, 128, 6, 32, 3, 3>(P, t, smem);
-    else rows_tile<FORM, EPI, 4, 128, 8, 32, 3, 3>(P, t, smem);
+// The slices' sums of the experts' rows, in order, and the epilogue: EPI and
+// GU as above (kSwiglu without GU: the gradient).  Eight columns a thread.
+template <bool GU, int EPI>
+__global__ void __launch_bounds__(256) k_rows_join(MmParams P) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8, size = (int64_t)P.M * P.C;
+    if (i >= size) return;
+    const int64_t row = i / P.C;
+    if (row < P.offsets[0] || row >= P.offsets[P.E]) return;
+    const auto sum = [&](int which, float (&v)[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+        for (int s = 0; s < P.slices; ++s) {
+            const float* p = P.part + (int64_t)(s * (GU ? 2 : 1) + which) * size + i;
+            const floatx4 a = *reinterpret_cast<const floatx4*>(p), b = *reinterpret_cast<const floatx4*>(p + 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[j] += a[j];
+                v[4 + j] += b[j];
+            }
+        }
+    };
+    const auto put = [&](uint16_t* o, const float (&v)[8]) {
+        *reinterpret_cast<uint4*>(o + i) = make_uint4(pack_rne(v[0], v[1]), pack_rne(v[2], v[3]), pack_rne(v[4], v[5]), pack_rne(v[6], v[7]));
+    };
+    float v[8];
+    sum(0, v);
+    if constexpr (GU) {
+        float u[8], h[8];
+        sum(1, u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] = v[j] * sigmoid(v[j]) * u[j];
+        put(P.o0, h);
+        if (P.o1) {
+            put(P.o1, v);
+            put(P.o2, u);
+        }
+    } else if constexpr (EPI == kSwiglu) {
+        const uint4 av = *reinterpret_cast<const uint4*>(P.i0 + i), bv = *reinterpret_cast<const uint4*>(P.i1 + i);
+        const floatx4 a[2] = {widen4(av.x, av.y), widen4(av.z, av.w)}, b[2] = {widen4(bv.x, bv.y), widen4(bv.z, bv.w)};
+        float da[8], db[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) swiglu_grad(v[j], a[j / 4][j % 4], b[j / 4][j % 4], da[j], db[j]);
+        put(P.o0, da);
+        put(P.o1, db);
+    } else {
+        put(P.o0, v);
+    }
 }
 
 // ---------------------------------------------------------------- weight gradient
@@ -681,35 +745,78 @@ __global__ void __launch_bounds__(256) k_wgrad_join(WgradParams P) {
 // tiles exist (one partial tile per expert); the ones beyond leave at once.
 int64_t row_tiles_bound(int M, int E, int BM) { return M / BM + (int64_t)std::min(E, M); }
 
-template <int FORM, int EPI, int BM>
+// How a row product of M rows of E experts runs: tiles of up to 64 or 256
+// rows (and two workgroups a CU of the former), and its reduction's slices.
+struct RowsPlan {
+    int bm, slices;
+    bool two;
+    size_t part_bytes;
+};
+
+// From the mean rows of an expert; the offsets are not known here.  A tile
+// goes through its reduction stage by stage (64 steps: 1.2 us for 256 rows;
+// for 64 rows 0.35 us with the other CUs quiet, 0.65 us with all of them
+// busy), so where tiles are few it is cut into slices, whose fp32 sums are
+// joined (4.5 TB/s, and another launch).  512 rows of one expert, 5120 x 512:
+// 106 us in two tiles, 47 us in 16, 17 us in 16 of 8 slices; 80 rows of two
+// experts, 5120 x 1536: 60 us whole, 17.6 us in slices; 8 experts of 256 rows,
+// 5120 x 1536, 105 us in 48 tiles and 55 us in 192 without slices.
+RowsPlan rows_plan(int M, int E, int R, int C, int pairs, int outs, int ntc) {
+    const int64_t experts = std::max(1, std::min(E, M)), mean = (M + experts - 1) / experts;
+    const int64_t t256 = experts * ((mean + 255) / 256) * ntc, t64 = experts * ((mean + 63) / 64) * ntc;
+    const int stages = (R + kBK - 1) / kBK * pairs;
+    RowsPlan best{mean > 48 ? 256 : 64, 1, mean <= 48, 0};
+    if ((mean > 48 ? t256 : t64) >= 256) return best;
+    double least = 1e30;
+    for (int bm = 64; bm <= 256; bm += 192) {
+        if (bm == 256 && mean <= 48) break;
+        const int64_t tiles = bm == 64 ? t64 : t256;
+        for (int n = 1; n <= 16; ++n) {
+            if (n > 1 && (n * 4 > stages || tiles * n > 512)) break;
+            // a short 256-tile costs what its rows do
+            const double stage = bm == 64 ? 0.35 + 0.3 * std::min(1.0, tiles * n / 256.0)
+                                          : 0.3 + 0.9 * std::min<double>(mean, 256) / 256;
+            const double bytes = (double)n * outs * M * C * 4;
+            const double us = (double)((tiles * n + 255) / 256) * ((stages + n - 1) / n) * stage +
+                              (n > 1 ? 4 + 2 * bytes / 4.5e6 : 0);
+            if (us < least) {
+                least = us;
+                best = RowsPlan{bm, n, false, n > 1 ? (size_t)bytes : 0};
+            }
+        }
+    }
+    return best;
+}
+
+template <int FORM, int EPI, int BM, int N64>
 moe_status launch_rows(const MmParams& P, const char* name, hipStream_t s) {
-    const int64_t grid = xcd_grid(row_tiles_bound(P.M, P.E, BM) * P.ntc);
-    constexpr size_t lds = BM == 64 ? rows_lds(64, 64, 2, 2) : rows_lds(256, 64, 2, 3);
+    const int64_t grid = xcd_grid(row_tiles_bound(P.M, P.E, BM) * P.ntc * (EPI == kPart ? P.slices : 1));
+    constexpr size_t lds = N64 == 2 ? rows_lds(64, 64, 2, 2) : rows_lds(256, 64, 2, 3);
     static_assert(rows_lds(256, 64, 2, 3) >= rows_lds(64, 64, 4, 4) && rows_lds(256, 64, 2, 3) >= rows_lds(128, 64, 3, 3),
                   "one size");
-    moe_status st = allow_dynamic_lds(reinterpret_cast<const void*>(&k_rows_mm<FORM, EPI, BM>), lds);
+    moe_status st = allow_dynamic_lds(reinterpret_cast<const void*>(&k_rows_mm<FORM, EPI, BM, N64>), lds);
     if (st != MOE_OK) return st;
-    MOE_LAUNCH(name, (k_rows_mm<FORM, EPI, BM>), dim3((unsigned)grid), dim3(kThreads), lds, s, P);
+    MOE_LAUNCH(name, (k_rows_mm<FORM, EPI, BM, N64>), dim3((unsigned)grid), dim3(kThreads), lds, s, P);
     return MOE_OK;
 }
 
 template <int FORM, int EPI>
-moe_status launch_rows4(const MmParams& P, const char* name, hipStream_t s) {
-    const int64_t grid = xcd_grid(row_tiles_bound(P.M, P.E, 128) * P.ntc);
-    constexpr size_t lds = rows_lds(128, 32, 3, 3);
-    moe_status st = allow_dynamic_lds(reinterpret_cast<const void*>(&k_rows_mm4<FORM, EPI>), lds);
-    if (st != MOE_OK) return st;
-    MOE_LAUNCH(name, (k_rows_mm4<FORM, EPI>), dim3((unsigned)grid), dim3(kThreads / 2), lds, s, P);
-    return MOE_OK;
+moe_status launch_rows_any(MmParams P, const char* name, void* ws, hipStream_t s) {
+    const RowsPlan p = rows_plan(P.M, P.E, P.R, P.C, P.pairs, FORM == kGateUp ? 2 : 1, P.ntc);
+    if (p.slices > 1) {
+        P.slices = p.slices;
+        P.part = static_cast<float*>(ws);
+        const moe_status st = p.bm == 64 ? launch_rows<FORM, kPart, 64, 4>(P, name, s) : launch_rows<FORM, kPart, 256, 4>(P, name, s);
+        if (st != MOE_OK) return st;
+        MOE_LAUNCH("grouped_join", (k_rows_join<FORM == kGateUp, EPI>), dim3((unsigned)(((int64_t)P.M * P.C + 2047) / 2048)),
+                   dim3(256), 0, s, P);
+        return MOE_OK;
+    }
+    if (p.two) return launch_rows<FORM, EPI, 64, 2>(P, name, s);
+    return p.bm == 64 ? launch_rows<FORM, EPI, 64, 4>(P, name, s) : launch_rows<FORM, EPI, 256, 4>(P, name, s);
 }
 
-template <int FORM, int EPI>
-moe_status launch_rows_any(const MmParams& P, const char* name, hipStream_t s) {
-    const int64_t mean = P.M / std::max(1, std::min(P.E, P.M));
-    if (mean > 48) return launch_rows<FORM, EPI, 256>(P, name, s);
-    if (mean > 48) return launch_rows4<FORM, EPI>(P, name, s);
-    return launch_rows<FORM, EPI, 64>(P, name, s);
-}
+int column_tiles(int C, bool gate_up) { return gate_up ? (C + kBN / 2 - 1) / (kBN / 2) : (C + kBN - 1) / kBN; }
 
 // Tile of a weight gradient and rows of a slice of its reduction.
 struct WgradPlan {
@@ -761,7 +868,11 @@ bool grouped_grid_fits(int M, int E, int C) {
 
 bool wgrad_grid_fits(int N, int K, int E) { return (int64_t)E * ((N + 127) / 128) * ((K + 127) / 128) < (1 << 22); }
 
-moe_status launch_grouped_fwd(const GroupedArgs& g, hipStream_t s) {
+size_t grouped_rows_workspace_bytes(int M, int E, int R, int C, int pairs, bool gate_up) {
+    return rows_plan(M, E, R, C, pairs, gate_up ? 2 : 1, column_tiles(C, gate_up)).part_bytes;
+}
+
+moe_status launch_grouped_fwd(const GroupedArgs& g, void* ws, hipStream_t s) {
     MmParams P{};
     P.a0 = g.x;
     P.w0 = g.w;
@@ -773,15 +884,12 @@ moe_status launch_grouped_fwd(const GroupedArgs& g, hipStream_t s) {
     P.R = g.K; P.C = g.N;
     P.pairs = 1;
     P.o0 = g.o0; P.o1 = g.o1; P.o2 = g.o2;
-    if (g.w2) {
-        P.ntc = (g.N + kBN / 2 - 1) / (kBN / 2);
-        return launch_rows_any<kNT, kSwiglu>(P, "grouped_swiglu", s);
-    }
-    P.ntc = (g.N + kBN - 1) / kBN;
-    return launch_rows_any<kNT, kPlain>(P, "grouped_linear", s);
+    P.ntc = column_tiles(g.N, g.w2 != nullptr);
+    if (g.w2) return launch_rows_any<kGateUp, kSwiglu>(P, "grouped_swiglu", ws, s);
+    return launch_rows_any<kNT, kPlain>(P, "grouped_linear", ws, s);
 }
 
-moe_status launch_grouped_dgrad(const GroupedArgs& g, hipStream_t s) {
+moe_status launch_grouped_dgrad(const GroupedArgs& g, void* ws, hipStream_t s) {
     MmParams P{};
     P.a0 = g.dy;
     P.a1 = g.dy2;
@@ -793,9 +901,9 @@ moe_status launch_grouped_dgrad(const GroupedArgs& g, hipStream_t s) {
     P.pairs = g.dy2 ? 2 : 1;
     P.o0 = g.o0; P.o1 = g.o1;
     P.i0 = g.a; P.i1 = g.b;
-    P.ntc = (g.K + kBN - 1) / kBN;
-    if (g.a) return launch_rows_any<kNN, kSwiglu>(P, "grouped_swiglu_dgrad", s);
-    return launch_rows_any<kNN, kPlain>(P, "grouped_dgrad", s);
+    P.ntc = column_tiles(g.K, false);
+    if (g.a) return launch_rows_any<kNN, kSwiglu>(P, "grouped_swiglu_dgrad", ws, s);
+    return launch_rows_any<kNN, kPlain>(P, "grouped_dgrad", ws, s);
 }
 
 size_t grouped_wgrad_workspace_bytes(int M, int N, int K, int E) {

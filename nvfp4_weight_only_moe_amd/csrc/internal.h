@@ -142,8 +142,10 @@ struct GroupedArgs {
 };
 bool grouped_grid_fits(int M, int E, int C);   // the launch of M rows and C output columns
 bool wgrad_grid_fits(int N, int K, int E);
-moe_status launch_grouped_fwd(const GroupedArgs& g, hipStream_t s);      // w2 set: gate/up with SwiGLU
-moe_status launch_grouped_dgrad(const GroupedArgs& g, hipStream_t s);    // a set: through SwiGLU
+// workspace of the row products: R the reduction's length, C the output columns
+size_t grouped_rows_workspace_bytes(int M, int E, int R, int C, int pairs, bool gate_up);
+moe_status launch_grouped_fwd(const GroupedArgs& g, void* ws, hipStream_t s);      // w2 set: gate/up with SwiGLU
+moe_status launch_grouped_dgrad(const GroupedArgs& g, void* ws, hipStream_t s);    // a set: through SwiGLU
 size_t grouped_wgrad_workspace_bytes(int M, int N, int K, int E);
 moe_status launch_grouped_wgrad(const GroupedArgs& g, float* dw, bool accumulate, void* ws, hipStream_t s);
 

@@ -28,21 +28,24 @@ def L():
 OK, ARG, SHAPE, ALIGN, UNSUP, WS = 0, -1, -2, -3, -4, -7
 
 
-def linear(L, x=at(0), X=8, K=64, w=at(1), E=4, N=32, off=at(2), slots=at(3), k=2, M=16, y=at(4)):
-    return L.moe_grouped_linear(x, X, K, w, E, N, off, slots, k, M, y, None)
+def linear(L, x=at(0), X=8, K=64, w=at(1), E=4, N=32, off=at(2), slots=at(3), k=2, M=16, y=at(4), ws=at(8),
+           ws_bytes=1 << 27):
+    return L.moe_grouped_linear(x, X, K, w, E, N, off, slots, k, M, y, ws, ws_bytes, None)
 
 
 def swiglu(L, x=at(0), X=8, K=64, g=at(1), u=at(2), E=4, N=32, off=at(3), slots=at(4), k=2, M=16, h=at(5), a=at(6),
-           bb=at(7)):
-    return L.moe_grouped_swiglu(x, X, K, g, u, E, N, off, slots, k, M, h, a, bb, None)
+           bb=at(7), ws=at(8), ws_bytes=1 << 27):
+    return L.moe_grouped_swiglu(x, X, K, g, u, E, N, off, slots, k, M, h, a, bb, ws, ws_bytes, None)
 
 
-def dgrad(L, dy=at(0), w=at(1), dy2=at(2), w2=at(3), M=16, N=32, E=4, K=64, off=at(4), dx=at(5)):
-    return L.moe_grouped_linear_dgrad(dy, w, dy2, w2, M, N, E, K, off, dx, None)
+def dgrad(L, dy=at(0), w=at(1), dy2=at(2), w2=at(3), M=16, N=32, E=4, K=64, off=at(4), dx=at(5), ws=at(8),
+          ws_bytes=1 << 27):
+    return L.moe_grouped_linear_dgrad(dy, w, dy2, w2, M, N, E, K, off, dx, ws, ws_bytes, None)
 
 
-def sdgrad(L, dy=at(0), w=at(1), M=16, N=32, E=4, K=64, off=at(2), a=at(3), bb=at(4), da=at(5), db=at(6)):
-    return L.moe_grouped_swiglu_dgrad(dy, w, M, N, E, K, off, a, bb, da, db, None)
+def sdgrad(L, dy=at(0), w=at(1), M=16, N=32, E=4, K=64, off=at(2), a=at(3), bb=at(4), da=at(5), db=at(6), ws=at(8),
+           ws_bytes=1 << 27):
+    return L.moe_grouped_swiglu_dgrad(dy, w, M, N, E, K, off, a, bb, da, db, ws, ws_bytes, None)
 
 
 def wgrad(L, dy=at(0), M=16, N=32, x=at(1), X=8, K=64, E=4, off=at(2), slots=at(3), k=2, acc=0, dw=at(4), ws=at(5),
@@ -79,6 +82,21 @@ def test_grouped_pointers(L):
     assert dgrad(L, dy2=0) == ARG and dgrad(L, w2=0) == ARG
     assert dgrad(L, dy2=at(9) + 8) == ALIGN
     assert dgrad(L, dx=at(2)) == ARG                                 # dx is dy2
+
+
+@pytest.mark.parametrize("f,products", [(linear, 1), (swiglu, 3), (dgrad, 2), (sdgrad, 1)])
+def test_grouped_workspace(L, f, products):
+    """Few rows and a long sum take a workspace: required, large enough, aligned, apart from every buffer."""
+    size = dict(M=16, N=64, K=8192, E=1) if f in (linear, swiglu) else dict(M=16, N=8192, K=64, E=1)
+    need = L.moe_grouped_workspace_size(16, 1, 8192, 64, products)
+    assert need >= 2 * 16 * 64 * 4
+    assert f(L, **size, ws=0) == WS and f(L, **size, ws_bytes=need - 1) == WS
+    assert f(L, **size, ws=at(8) + 8) == ALIGN
+    for i in range(5):
+        assert f(L, **size, ws=at(i)) == ARG, i
+    assert L.moe_grouped_workspace_size(0, 1, 8192, 64, products) == 0
+    assert L.moe_grouped_workspace_size(16, 1, 8192, 64, 4) == 0
+    assert L.moe_grouped_workspace_size(1 << 20, 64, 4096, 4096, products) == 0    # many tiles: none
 
 
 @pytest.mark.parametrize("f", [linear, swiglu, wgrad])

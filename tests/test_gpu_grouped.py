@@ -271,5 +271,5 @@ def test_gathered_rows_past_the_offset_range_are_refused():
     L = B.lib()
     out = torch.empty((1, 8), dtype=BF, device=DEV)
     st = L.moe_grouped_linear(x.data_ptr(), 4096, 1 << 20, w.data_ptr(), 1, 8, off.data_ptr(), slots.data_ptr(), 1, 1,
-                              out.data_ptr(), None)
+                              out.data_ptr(), None, 0, None)
     assert B.STATUS[st] == "MOE_ERR_SHAPE"
