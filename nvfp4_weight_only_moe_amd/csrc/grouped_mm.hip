@@ -501,7 +501,8 @@ __global__ void __launch_bounds__(kThreads, N64 == 2 ? 4 : 2) k_rows_mm(MmParams
         else if (t.rows <= 128) rows_tile<FORM, EPI, 8, 128, 4, 64, 3, 3>(P, t, smem);
         else if (t.rows <= 160) rows_tile<FORM, EPI, 8, 192, 5, 64, 2, 3>(P, t, smem);
         else if (t.rows <= 192) rows_tile<FORM, EPI, 8, 192, 6, 64, 2, 3>(P, t, smem);
-        else rows_tile<FORM, EPI, 8, 256, 8, 64, 2, 3>(P, t, smem);
+        else if (t.rows <= 256) rows_tile<FORM, EPI, 8, 256, 8, 64, 2, 3>(P, t, smem);
+        else rows_tile<FORM, EPI, 8, 320, 9, 64, 2, 2>(P, t, smem);
     }
 }
 
@@ -755,7 +756,7 @@ struct RowsPlan {
 
 // From the mean rows of an expert; the offsets are not known here.  A tile
 // goes through its reduction stage by stage (64 steps: 1.2 us for 256 rows;
-// for 64 rows 0.35 us with the other CUs quiet, 0.65 us with all of them
+// for 64 rows 0.5 us with the other CUs quiet, 0.65 us with all of them
 // busy), so where tiles are few it is cut into slices, whose fp32 sums are
 // joined (4.5 TB/s, and another launch).  512 rows of one expert, 5120 x 512:
 // 106 us in two tiles, 47 us in 16, 17 us in 16 of 8 slices; 80 rows of two
@@ -774,7 +775,7 @@ RowsPlan rows_plan(int M, int E, int R, int C, int pairs, int outs, int ntc) {
         for (int n = 1; n <= 16; ++n) {
             if (n > 1 && (n * 4 > stages || tiles * n > 512)) break;
             // a short 256-tile costs what its rows do
-            const double stage = bm == 64 ? 0.35 + 0.3 * std::min(1.0, tiles * n / 256.0)
+            const double stage = bm == 64 ? 0.5 + 0.15 * std::min(1.0, tiles * n / 256.0)
                                           : 0.3 + 0.9 * std::min<double>(mean, 256) / 256;
             const double bytes = (double)n * outs * M * C * 4;
             const double us = (double)((tiles * n + 255) / 256) * ((stages + n - 1) / n) * stage +
@@ -806,14 +807,14 @@ moe_status launch_rows_any(MmParams P, const char* name, void* ws, hipStream_t s
     if (p.slices > 1) {
         P.slices = p.slices;
         P.part = static_cast<float*>(ws);
-        const moe_status st = p.bm == 64 ? launch_rows<FORM, kPart, 64, 4>(P, name, s) : launch_rows<FORM, kPart, 256, 4>(P, name, s);
+        const moe_status st = p.bm == 64 ? launch_rows<FORM, kPart, 64, 4>(P, name, s) : launch_rows<FORM, kPart, 288, 4>(P, name, s);
         if (st != MOE_OK) return st;
         MOE_LAUNCH("grouped_join", (k_rows_join<FORM == kGateUp, EPI>), dim3((unsigned)(((int64_t)P.M * P.C + 2047) / 2048)),
                    dim3(256), 0, s, P);
         return MOE_OK;
     }
     if (p.two) return launch_rows<FORM, EPI, 64, 2>(P, name, s);
-    return p.bm == 64 ? launch_rows<FORM, EPI, 64, 4>(P, name, s) : launch_rows<FORM, EPI, 256, 4>(P, name, s);
+    return p.bm == 64 ? launch_rows<FORM, EPI, 64, 4>(P, name, s) : launch_rows<FORM, EPI, 288, 4>(P, name, s);
 }
 
 int column_tiles(int C, bool gate_up) { return gate_up ? (C + kBN / 2 - 1) / (kBN / 2) : (C + kBN - 1) / kBN; }
