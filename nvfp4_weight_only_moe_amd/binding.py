@@ -616,7 +616,9 @@ def _rows(x, sorted_slots):
 GROUPED_ONE, GROUPED_PAIR, GROUPED_SWIGLU = 1, 2, 3
 
 
+@functools.lru_cache(maxsize=4096)
 def moe_grouped_workspace_size(M, E, R, C, products=GROUPED_ONE):
+    """Workspace bytes of a grouped product (a function of its sizes alone)."""
     return int(lib().moe_grouped_workspace_size(M, E, R, C, products))
 
 
@@ -624,7 +626,7 @@ def _workspace(ws, need, like):
     """(address, bytes) of a workspace of at least `need` bytes on `like`'s
     device (allocated if None), and the tensor, to be kept until the launch."""
     if ws is None:
-        if need == 0:
+        if not need:
             return None, 0, None
         ws = like.new_empty((need,), dtype=torch.uint8)
     _dev_tensor(ws, "ws", min_bytes=need)
@@ -644,7 +646,7 @@ def moe_grouped_linear(x, w, offsets, sorted_slots=None, k=1, out=None, ws=None)
     M, ps = _rows(x, sorted_slots)
     out = _new(out, "out", x, x.dtype, (M, N))
     L = lib()
-    pws, nws, ws = _workspace(ws, L.moe_grouped_workspace_size(M, E, K, N, GROUPED_ONE), x)
+    pws, nws, ws = _workspace(ws, moe_grouped_workspace_size(M, E, K, N, GROUPED_ONE), x)
     _check(L.moe_grouped_linear(px, X, K, pw, E, N, po, ps, k, M, out.data_ptr(), pws, nws, _here(x)),
            "moe_grouped_linear")
     return out
@@ -666,7 +668,7 @@ def moe_grouped_swiglu(x, gate, up, offsets, sorted_slots=None, k=1, h=None, a=N
     if save:
         a, b = _new(a, "a", x, x.dtype, (M, N)), _new(b, "b", x, x.dtype, (M, N))
     L = lib()
-    pws, nws, ws = _workspace(ws, L.moe_grouped_workspace_size(M, E, K, N, GROUPED_SWIGLU), x)
+    pws, nws, ws = _workspace(ws, moe_grouped_workspace_size(M, E, K, N, GROUPED_SWIGLU), x)
     _check(L.moe_grouped_swiglu(px, X, K, pg, pu, E, N, po, ps, k, M, h.data_ptr(), a.data_ptr() if save else None,
                                 b.data_ptr() if save else None, pws, nws, _here(x)), "moe_grouped_swiglu")
     return (h, a, b) if save else h
@@ -686,7 +688,7 @@ def moe_grouped_linear_dgrad(dy, w, offsets, dy2=None, w2=None, out=None, ws=Non
         pd2, pw2 = _same(dy2, "dy2", dy, _BITS16, (M, N)), _same(w2, "w2", dy, _BITS16, (E, N, K))
     out = _new(out, "out", dy, dy.dtype, (M, K))
     L = lib()
-    pws, nws, ws = _workspace(ws, L.moe_grouped_workspace_size(M, E, N, K, GROUPED_ONE if dy2 is None else GROUPED_PAIR),
+    pws, nws, ws = _workspace(ws, moe_grouped_workspace_size(M, E, N, K, GROUPED_ONE if dy2 is None else GROUPED_PAIR),
                               dy)
     _check(L.moe_grouped_linear_dgrad(pd, pw, pd2, pw2, M, N, E, K, po, out.data_ptr(), pws, nws, _here(dy)),
            "moe_grouped_linear_dgrad")
@@ -703,7 +705,7 @@ def moe_grouped_swiglu_dgrad(dy, w, a, b, offsets, da=None, db=None, ws=None):
     po = _same(offsets, "offsets", dy, _I32, (E + 1,))
     da, db = _new(da, "da", dy, dy.dtype, (M, K)), _new(db, "db", dy, dy.dtype, (M, K))
     L = lib()
-    pws, nws, ws = _workspace(ws, L.moe_grouped_workspace_size(M, E, N, K, GROUPED_ONE), dy)
+    pws, nws, ws = _workspace(ws, moe_grouped_workspace_size(M, E, N, K, GROUPED_ONE), dy)
     _check(L.moe_grouped_swiglu_dgrad(pd, pw, M, N, E, K, po, pa, pb, da.data_ptr(), db.data_ptr(), pws, nws, _here(dy)),
            "moe_grouped_swiglu_dgrad")
     return da, db
@@ -725,13 +727,15 @@ def moe_grouped_linear_wgrad(dy, x, offsets, sorted_slots=None, k=1, out=None, a
         raise ValueError("accumulate needs out")
     out = _new(out, "out", dy, torch.float32, (E, N, K))
     L = lib()
-    pws, nws, ws = _workspace(ws, L.moe_grouped_linear_wgrad_workspace_size(M, N, K, E), dy)
+    pws, nws, ws = _workspace(ws, moe_grouped_linear_wgrad_workspace_size(M, N, K, E), dy)
     _check(L.moe_grouped_linear_wgrad(pd, M, N, px, X, K, E, po, ps, k, int(bool(accumulate)), out.data_ptr(), pws, nws,
                                       _here(dy)), "moe_grouped_linear_wgrad")
     return out
 
 
+@functools.lru_cache(maxsize=4096)
 def moe_grouped_linear_wgrad_workspace_size(M, N, K, E):
+    """Workspace bytes of a weight gradient (a function of its sizes alone)."""
     return int(lib().moe_grouped_linear_wgrad_workspace_size(M, N, K, E))
 
 

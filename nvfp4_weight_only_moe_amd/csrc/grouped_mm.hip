@@ -487,15 +487,14 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
 // Tiles of up to BM rows, by their rows: a short tile waits for memory, not
 // for the matrix units, and its smaller stages leave room for more of them in
 // flight.  The weights, which come from HBM, have a stage more in flight than
-// the rows, which come from L2.  N64: stages of a 64-row tile in LDS, 4, or 2
-// for two workgroups a CU.
-template <int FORM, int EPI, int BM, int N64>
-__global__ void __launch_bounds__(kThreads, N64 == 2 ? 4 : 2) k_rows_mm(MmParams P) {
+// the rows, which come from L2.
+template <int FORM, int EPI, int BM>
+__global__ void __launch_bounds__(kThreads, 2) k_rows_mm(MmParams P) {
     extern __shared__ __align__(16) uint8_t smem[];
     const RowTile t = find_tile<BM, EPI == kPart>(P, blockIdx.x);
     if (t.e < 0) return;
-    if (t.rows <= 32) rows_tile<FORM, EPI, 8, 64, 1, 64, N64, N64>(P, t, smem);
-    else if (BM == 64 || t.rows <= 64) rows_tile<FORM, EPI, 8, 64, 2, 64, N64, N64>(P, t, smem);
+    if (t.rows <= 32) rows_tile<FORM, EPI, 8, 64, 1, 64, 4, 4>(P, t, smem);
+    else if (BM == 64 || t.rows <= 64) rows_tile<FORM, EPI, 8, 64, 2, 64, 4, 4>(P, t, smem);
     else if constexpr (BM > 64) {
         if (t.rows <= 96) rows_tile<FORM, EPI, 8, 128, 3, 64, 3, 3>(P, t, smem);
         else if (t.rows <= 128) rows_tile<FORM, EPI, 8, 128, 4, 64, 3, 3>(P, t, smem);
@@ -746,11 +745,10 @@ __global__ void __launch_bounds__(256) k_wgrad_join(WgradParams P) {
 // tiles exist (one partial tile per expert); the ones beyond leave at once.
 int64_t row_tiles_bound(int M, int E, int BM) { return M / BM + (int64_t)std::min(E, M); }
 
-// How a row product of M rows of E experts runs: tiles of up to 64 or 256
-// rows (and two workgroups a CU of the former), and its reduction's slices.
+// How a row product of M rows of E experts runs: tiles of up to 64 or 288
+// rows, and its reduction's slices.
 struct RowsPlan {
     int bm, slices;
-    bool two;
     size_t part_bytes;
 };
 
@@ -764,40 +762,40 @@ struct RowsPlan {
 // 5120 x 1536, 105 us in 48 tiles and 55 us in 192 without slices.
 RowsPlan rows_plan(int M, int E, int R, int C, int pairs, int outs, int ntc) {
     const int64_t experts = std::max(1, std::min(E, M)), mean = (M + experts - 1) / experts;
-    const int64_t t256 = experts * ((mean + 255) / 256) * ntc, t64 = experts * ((mean + 63) / 64) * ntc;
+    const int64_t t288 = experts * ((mean + 287) / 288) * ntc, t64 = experts * ((mean + 63) / 64) * ntc;
     const int stages = (R + kBK - 1) / kBK * pairs;
-    RowsPlan best{mean > 48 ? 256 : 64, 1, mean <= 48, 0};
-    if ((mean > 48 ? t256 : t64) >= 256) return best;
+    RowsPlan best{mean > 48 ? 288 : 64, 1, 0};
+    if ((mean > 48 ? t288 : t64) >= 256) return best;
     double least = 1e30;
-    for (int bm = 64; bm <= 256; bm += 192) {
-        if (bm == 256 && mean <= 48) break;
-        const int64_t tiles = bm == 64 ? t64 : t256;
+    for (const int bm : {64, 288}) {
+        if (bm == 288 && mean <= 48) break;
+        const int64_t tiles = bm == 64 ? t64 : t288;
         for (int n = 1; n <= 16; ++n) {
             if (n > 1 && (n * 4 > stages || tiles * n > 512)) break;
-            // a short 256-tile costs what its rows do
+            // a short 288-tile costs what its rows do
             const double stage = bm == 64 ? 0.5 + 0.15 * std::min(1.0, tiles * n / 256.0)
-                                          : 0.3 + 0.9 * std::min<double>(mean, 256) / 256;
+                                          : 0.3 + 0.9 * std::min<double>(mean, 288) / 256;
             const double bytes = (double)n * outs * M * C * 4;
             const double us = (double)((tiles * n + 255) / 256) * ((stages + n - 1) / n) * stage +
                               (n > 1 ? 4 + 2 * bytes / 4.5e6 : 0);
             if (us < least) {
                 least = us;
-                best = RowsPlan{bm, n, false, n > 1 ? (size_t)bytes : 0};
+                best = RowsPlan{bm, n, n > 1 ? (size_t)bytes : 0};
             }
         }
     }
     return best;
 }
 
-template <int FORM, int EPI, int BM, int N64>
+template <int FORM, int EPI, int BM>
 moe_status launch_rows(const MmParams& P, const char* name, hipStream_t s) {
     const int64_t grid = xcd_grid(row_tiles_bound(P.M, P.E, BM) * P.ntc * (EPI == kPart ? P.slices : 1));
-    constexpr size_t lds = N64 == 2 ? rows_lds(64, 64, 2, 2) : rows_lds(256, 64, 2, 3);
-    static_assert(rows_lds(256, 64, 2, 3) >= rows_lds(64, 64, 4, 4) && rows_lds(256, 64, 2, 3) >= rows_lds(128, 64, 3, 3),
+    constexpr size_t lds = rows_lds(256, 64, 2, 3);
+    static_assert(rows_lds(64, 64, 4, 4) <= lds && rows_lds(128, 64, 3, 3) <= lds && rows_lds(320, 64, 2, 2) <= lds,
                   "one size");
-    moe_status st = allow_dynamic_lds(reinterpret_cast<const void*>(&k_rows_mm<FORM, EPI, BM, N64>), lds);
+    moe_status st = allow_dynamic_lds(reinterpret_cast<const void*>(&k_rows_mm<FORM, EPI, BM>), lds);
     if (st != MOE_OK) return st;
-    MOE_LAUNCH(name, (k_rows_mm<FORM, EPI, BM, N64>), dim3((unsigned)grid), dim3(kThreads), lds, s, P);
+    MOE_LAUNCH(name, (k_rows_mm<FORM, EPI, BM>), dim3((unsigned)grid), dim3(kThreads), lds, s, P);
     return MOE_OK;
 }
 
@@ -807,14 +805,13 @@ moe_status launch_rows_any(MmParams P, const char* name, void* ws, hipStream_t s
     if (p.slices > 1) {
         P.slices = p.slices;
         P.part = static_cast<float*>(ws);
-        const moe_status st = p.bm == 64 ? launch_rows<FORM, kPart, 64, 4>(P, name, s) : launch_rows<FORM, kPart, 288, 4>(P, name, s);
+        const moe_status st = p.bm == 64 ? launch_rows<FORM, kPart, 64>(P, name, s) : launch_rows<FORM, kPart, 288>(P, name, s);
         if (st != MOE_OK) return st;
         MOE_LAUNCH("grouped_join", (k_rows_join<FORM == kGateUp, EPI>), dim3((unsigned)(((int64_t)P.M * P.C + 2047) / 2048)),
                    dim3(256), 0, s, P);
         return MOE_OK;
     }
-    if (p.two) return launch_rows<FORM, EPI, 64, 2>(P, name, s);
-    return p.bm == 64 ? launch_rows<FORM, EPI, 64, 4>(P, name, s) : launch_rows<FORM, EPI, 288, 4>(P, name, s);
+    return p.bm == 64 ? launch_rows<FORM, EPI, 64>(P, name, s) : launch_rows<FORM, EPI, 288>(P, name, s);
 }
 
 int column_tiles(int C, bool gate_up) { return gate_up ? (C + kBN / 2 - 1) / (kBN / 2) : (C + kBN - 1) / kBN; }

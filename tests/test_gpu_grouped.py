@@ -17,6 +17,11 @@ CASES = [
     ([1], 8, 8), ([1], 64, 16), ([3, 0, 1], 72, 40), ([0, 0, 5], 256, 128), ([17, 64, 65, 0], 136, 264),
     ([127, 128, 129], 264, 72), ([255, 256, 257, 1], 200, 520), ([600, 2, 0, 31], 320, 256),
     ([2] * 70 + [0] * 30 + [1] * 30, 128, 64), ([40] * 3, 1032, 1024), ([300], 64, 1288),
+    # many tiles of every height (one to nine 16-row subtiles a wave), each way
+    ([255, 256, 257, 288, 289, 190, 170, 130, 96, 80, 64, 33, 17, 1, 0] * 4, 72, 1288),
+    ([288, 240, 161, 96, 1] * 8, 1800, 72), ([3] * 200 + [0] * 40, 80, 520),
+    # few rows and a long sum: slices, also across the two products of a pair
+    ([5, 0, 70], 4104, 136), ([90], 136, 4104),
 ]
 IDS = [f"{len(c)}x{max(c)}-K{k}-N{n}" for c, k, n in CASES]
 
@@ -145,8 +150,9 @@ def wgrad_ref(dy, rows, off, N, K):
 
 
 @pytest.mark.parametrize("pad", [0, 3])
-@pytest.mark.parametrize("counts,K,N", CASES + [([5000], 136, 72), ([3000, 1, 2500], 64, 264)],
-                         ids=IDS + ["1x5000", "3x3000"])
+@pytest.mark.parametrize("counts,K,N", CASES + [([5000], 136, 72), ([3000, 1, 2500], 64, 264), ([700, 200, 400], 136, 256),
+                                                  ([4999], 72, 512)],
+                         ids=IDS + ["1x5000", "3x3000", "3x700", "1x4999"])
 def test_wgrad(counts, K, N, pad):
     g, off, M, live = problem(counts, K, N, pad, seed=4)
     dy, x = with_nan(randn(g, M, N), live), with_nan(randn(g, M, K), live)
@@ -162,7 +168,7 @@ def test_wgrad(counts, K, N, pad):
     assert (got[empty] == 0).all() and torch.equal(acc[empty], before[empty])
 
 
-@pytest.mark.parametrize("counts,K,N", CASES + [([5000], 136, 72)], ids=IDS + ["1x5000"])
+@pytest.mark.parametrize("counts,K,N", CASES + [([5000], 136, 72), ([4999, 1100], 264, 512)], ids=IDS + ["1x5000", "2x4999"])
 @pytest.mark.parametrize("k", [1, 7])
 def test_wgrad_gathered(counts, K, N, k):
     g, off, M, live = problem(counts, K, N, seed=5 + k)
