@@ -550,7 +550,7 @@ def _entry(fn):
         if dev < 0:
             raise ValueError(f"{fn.__name__}: expected a device (cuda) tensor, got {first.device}")
         if stream is None:
-            if dev == torch.cuda.current_device():
+            if dev == _current_device():
                 return fn(first, *args, **kw)
             with torch.cuda.device(dev):
                 return fn(first, *args, **kw)
@@ -601,7 +601,9 @@ def _here(t):
     return _raw_stream(t.get_device())
 
 
-# torch.cuda.current_stream() builds an object for the same answer (2.8 us against 0.1)
+# torch.cuda.current_stream() builds an object for the same answer (2.8 us
+# against 0.1), torch.cuda.current_device() initialises first (0.26)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
 
 
@@ -763,17 +765,15 @@ class Int4Tensor:
         return self.shape[2] // max(self.scales.shape[-1], 1)
 
     def cstruct(self, like=None):
-        like = self.codes if like is None else like
-        _dims(self.codes, "codes", 3)
-        _dims(self.scales, "scales", 3)
-        E, N, K = self.shape
-        groups = self.scales.shape[-1]
+        codes, scales, zeros = self.codes, self.scales, self.zeros
+        like = codes if like is None else like
+        (E, N, half), (_, _, groups) = _dims(codes, "codes", 3), _dims(scales, "scales", 3)
+        K = half * 2
         if groups < 1 or K % groups:
             raise ValueError(f"scales: {groups} groups for {K} columns")
-        pc = _same(self.codes, "codes", like, _U8, (E, N, K // 2))
-        ps = _same(self.scales, "scales", like, _BITS16, (E, N, groups))
-        pz = None if self.zeros is None else _same(self.zeros, "zeros", like, _U8, (E, N, groups))
-        return Int4TensorC(E, N, K, K // groups, pc, ps, pz)
+        return Int4TensorC(E, N, K, K // groups, _same(codes, "codes", like, _U8, (E, N, half)),
+                           _same(scales, "scales", like, _BITS16, (E, N, groups)),
+                           None if zeros is None else _same(zeros, "zeros", like, _U8, (E, N, groups)))
 
     @staticmethod
     def empty(E, N, K, group=128, zeros=True, device="cuda"):
