@@ -484,8 +484,11 @@ moe_status moe_int4_dequantize(const moe_int4_tensor *t, float *d_w_out, hipStre
  * products exact and accumulated in fp32, no weight rounded.
  *   d_offsets NULL: a dense projection of x [X][K], E == 1, X == M, no sorted
  *   slots; given: rows by expert, with d_sorted_slots as in moe_grouped_linear.
- *   d_out bf16 [M][N].  Any N; M == 0 is a no-op.  Weights are streamed once
- *   per block of rows: the form for decode.  Deterministic; graph-capturable.
+ *   d_out bf16 [M][N].  Any N; M == 0 is a no-op; MOE_ERR_SHAPE from 2^22
+ *   blocks of up to 64 rows by up to 128 columns.  The sums are formed as
+ *   (128 + code) x less (128 + zero) x: an infinite x gives NaN.  Weights are
+ *   streamed once per block of rows: the form for decode.  Deterministic;
+ *   graph-capturable.
  */
 moe_status moe_int4_linear(const uint16_t *d_x, int32_t X, const moe_int4_tensor *w, const int32_t *d_offsets,
                            const int32_t *d_sorted_slots, int32_t k, int32_t M, uint16_t *d_out,
@@ -507,7 +510,7 @@ moe_status moe_int4_linear(const uint16_t *d_x, int32_t X, const moe_int4_tensor
  *   names are not written.
  *   d_w fp32 [T][k], or NULL: all 1.  d_dw and d_dlogits may be NULL (y is
  *   then not read); d_dlogits needs d_w and d_topk_ids (int32 [T][k]).
- *   H % 8 == 0, k <= 32, T <= 2^23.  T == 0 is a no-op.  Sums in fp32 in slot
+ *   H % 8 == 0, k <= 32, T <= 2^22.  T == 0 is a no-op.  Sums in fp32 in slot
  *   order; deterministic; graph-capturable.
  */
 moe_status moe_combine(const uint16_t *d_y, int32_t M, int32_t H, const int32_t *d_slot_pos, const float *d_w,

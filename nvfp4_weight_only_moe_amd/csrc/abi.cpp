@@ -64,15 +64,22 @@ bool prof_events(const char* name, hipEvent_t* start, hipEvent_t* stop) {
 }
 
 moe_status allow_dynamic_lds(const void* kernel, size_t bytes) {
+    struct Done {
+        const void* kernel;
+        int device;
+        size_t bytes;
+    };
     static std::mutex mu;
-    static std::vector<std::pair<const void*, size_t>> done;
+    static std::vector<Done> done;
+    int device = 0;
+    if (hipGetDevice(&device) != hipSuccess) return MOE_ERR_HIP;
     std::lock_guard<std::mutex> lk(mu);
     for (auto& d : done)
-        if (d.first == kernel && d.second >= bytes) return MOE_OK;
+        if (d.kernel == kernel && d.device == device && d.bytes >= bytes) return MOE_OK;
     if (bytes > 64 * 1024 &&
         hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != hipSuccess)
         return MOE_ERR_HIP;
-    done.emplace_back(kernel, bytes);
+    done.push_back(Done{kernel, device, bytes});
     return MOE_OK;
 }
 

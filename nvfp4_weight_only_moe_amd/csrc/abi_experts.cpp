@@ -254,7 +254,7 @@ moe_status moe_int4_linear(const uint16_t* d_x, int32_t X, const moe_int4_tensor
 
 moe_status moe_combine(const uint16_t* d_y, int32_t M, int32_t H, const int32_t* d_slot_pos, const float* d_w,
                        int32_t T, int32_t k, uint16_t* d_out, hipStream_t stream) {
-    if (T < 0 || M < 0 || k < 1 || H < 8 || H % 8 || H > kMaxDim || T > (1 << 23) || M > kMaxRows) return MOE_ERR_SHAPE;
+    if (T < 0 || M < 0 || k < 1 || H < 8 || H % 8 || H > kMaxDim || T > (1 << 22) || M > kMaxRows) return MOE_ERR_SHAPE;
     if (k > MOE_MAX_TOPK) return MOE_ERR_UNSUPPORTED;
     if (T == 0) return MOE_OK;
     const Buf y{d_y, b16(M, H)}, pos{d_slot_pos, (size_t)T * k * 4}, w{d_w, (size_t)T * k * 4}, out{d_out, b16(T, H)};
@@ -269,7 +269,7 @@ moe_status moe_combine(const uint16_t* d_y, int32_t M, int32_t H, const int32_t*
 moe_status moe_combine_backward(const uint16_t* d_dout, int32_t T, int32_t H, const uint16_t* d_y, int32_t M,
                                 const int32_t* d_slot_pos, const float* d_w, const int32_t* d_topk_ids, int32_t k,
                                 int32_t E, uint16_t* d_dy, float* d_dw, float* d_dlogits, hipStream_t stream) {
-    if (T < 0 || M < 0 || k < 1 || H < 8 || H % 8 || H > kMaxDim || T > (1 << 23) || M > kMaxRows) return MOE_ERR_SHAPE;
+    if (T < 0 || M < 0 || k < 1 || H < 8 || H % 8 || H > kMaxDim || T > (1 << 22) || M > kMaxRows) return MOE_ERR_SHAPE;
     if (k > MOE_MAX_TOPK) return MOE_ERR_UNSUPPORTED;
     if (d_dlogits) {
         if (E < 1) return MOE_ERR_SHAPE;

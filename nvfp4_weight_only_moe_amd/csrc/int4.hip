@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kVecWaves * kWave, 4) k_int4_vec(Int4Params P,
         }
 #pragma unroll
         for (int r = 0; r < kVecRows / 2; ++r) {
-            const float s = bf16_bits_to_f32(sc[r]), off = -128.0f - (float)zp[r];
+            const float s = in ? bf16_bits_to_f32(sc[r]) : 0.0f, off = -128.0f - (float)zp[r];
             const uint32_t cw[4] = {codes[r].x, codes[r].y, codes[r].z, codes[r].w};
             float dot[T];
 #pragma unroll
@@ -447,6 +447,7 @@ moe_status launch_int4_z(Int4Params P, hipStream_t s) {
     constexpr int NR = 16 * RT * WR, TOK = 16 * TT;
     P.ntn = (P.N + NR - 1) / NR;
     const int64_t blocks = P.offsets ? P.M / TOK + (int64_t)std::min(P.E, P.M) : (P.M + TOK - 1) / TOK;
+    if (blocks * P.ntn >= (1 << 22)) return MOE_ERR_SHAPE;
     const size_t lds = Int4Lds<RT, TT>::kBytes;
     moe_status st = allow_dynamic_lds(reinterpret_cast<const void*>(&k_int4_mm<G, RT, TT, WR, ZP>), lds);
     if (st != MOE_OK) return st;

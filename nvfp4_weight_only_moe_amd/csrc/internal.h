@@ -30,7 +30,7 @@ bool prof_events(const char* name, hipEvent_t* start, hipEvent_t* stop);
     } while (0)
 
 // Allow `bytes` of dynamic LDS for `kernel` (HIP needs an explicit opt-in
-// above 64 KB).  Cached per kernel; host-side only, never captured.
+// above 64 KB).  Cached per kernel and device; host-side only, never captured.
 moe_status allow_dynamic_lds(const void* kernel, size_t bytes);
 
 // ---- quantize.hip

@@ -139,6 +139,7 @@ def test_int4(L):
     assert int4(L, K=192) == SHAPE and int4(L, group=16) == SHAPE and int4(L, N=0) == SHAPE and int4(L, E=0) == SHAPE
     assert int4(L, E=1025, off=at(4)) == UNSUP
     assert int4(L, M=-1) == SHAPE and int4(L, M=5) == SHAPE          # X == M
+    assert int4(L, M=1 << 29, X=1 << 29, out=1 << 60) == SHAPE         # more than 2^22 tiles
     assert int4(L, E=2) == ARG                                       # experts need offsets
     assert int4(L, slots=at(4)) == ARG                               # slots need offsets
     assert int4(L, off=at(4) + 4) == ALIGN
@@ -173,7 +174,7 @@ def test_combine_shapes(L, f):
     assert f(L, T=0) == OK
     assert f(L, T=-1) == SHAPE and f(L, M=-1) == SHAPE and f(L, k=0) == SHAPE
     assert f(L, H=60) == SHAPE and f(L, H=0) == SHAPE and f(L, H=(1 << 20) + 8) == SHAPE
-    assert f(L, T=(1 << 23) + 1) == SHAPE and f(L, k=33) == UNSUP
+    assert f(L, T=(1 << 22) + 1) == SHAPE and f(L, k=33) == UNSUP
 
 
 def test_combine_pointers(L):

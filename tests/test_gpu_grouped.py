@@ -22,6 +22,7 @@ CASES = [
     ([288, 240, 161, 96, 1] * 8, 1800, 72), ([3] * 200 + [0] * 40, 80, 520),
     # few rows and a long sum: slices, also across the two products of a pair
     ([5, 0, 70], 4104, 136), ([90], 136, 4104),
+    ([1, 0, 2, 0] * 256, 64, 40),                         # as many experts as there may be
 ]
 IDS = [f"{len(c)}x{max(c)}-K{k}-N{n}" for c, k, n in CASES]
 
