@@ -429,9 +429,30 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
     // One rounding to bf16 per output; a lane stores eight columns of one row.
     // Every lane takes part in the exchanges, also those that store nothing.
     constexpr int kPairs = GU ? 1 : 2;
+    // The saved a and b: those of kAhead subtiles requested at once, in the
+    // registers that the fragments leave (one at a time, each behind the
+    // stores before it, 32 experts of 255 rows took FIG us more).
+    constexpr bool kGrad = FORM == kNN && EPI == kSwiglu;
+    constexpr int kAhead = U > 8 ? 3 : 4;
+    uint4 asave[kGrad ? kAhead : 1][kPairs], bsave[kGrad ? kAhead : 1][kPairs];
 #pragma unroll
     for (int mi = 0; mi < U; ++mi) {
         const int r = (mi * WM + wm) * 16 + lrow;
+        if constexpr (kGrad) {
+            if (mi % kAhead == 0)
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+                    for (int j = 0; j < kPairs; ++j) {
+                        // lanes outside read the tile's last row or columns, so
+                        // that no load waits behind a branch
+                        const int ra = min(((mi + i) * WM + wm) * 16 + lrow, t.rows - 1);
+                        const int ca = min(c0 + wn * 64 + j * 32 + (q & 1) * 16 + (q >> 1) * 8, P.C - 8);
+                        const int64_t at = (int64_t)(t.p0 + ra) * P.C + ca;
+                        asave[i][j] = *reinterpret_cast<const uint4*>(P.i0 + at);
+                        bsave[i][j] = *reinterpret_cast<const uint4*>(P.i1 + at);
+                    }
+        }
         const int64_t row = (int64_t)(t.p0 + r) * P.C;
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
@@ -453,11 +474,7 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
                     }
                 }
             } else if constexpr (EPI == kSwiglu) {
-                // lanes outside read the tile's last row or columns, so that no
-                // load waits behind a branch
-                const int64_t at = (int64_t)(t.p0 + min(r, t.rows - 1)) * P.C + min(c, P.C - 8);
-                uint4 av = *reinterpret_cast<const uint4*>(P.i0 + at), bv = *reinterpret_cast<const uint4*>(P.i1 + at);
-                const Pair4 ap = exchange_back(av), bp = exchange_back(bv);
+                const Pair4 ap = exchange_back(asave[mi % kAhead][j]), bp = exchange_back(bsave[mi % kAhead][j]);
                 const floatx4 a[2] = {widen4(ap.a0, ap.a1), widen4(ap.b0, ap.b1)};
                 const floatx4 b[2] = {widen4(bp.a0, bp.a1), widen4(bp.b0, bp.b1)};
                 floatx4 da[2], db[2];
@@ -470,8 +487,7 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
                         da[n][i] = x;
                         db[n][i] = y;
                     }
-                av = pack_pair(da[0], da[1]);
-                bv = pack_pair(db[0], db[1]);
+                const uint4 av = pack_pair(da[0], da[1]), bv = pack_pair(db[0], db[1]);
                 if (ok) {
                     *reinterpret_cast<uint4*>(P.o0 + row + c) = av;
                     *reinterpret_cast<uint4*>(P.o1 + row + c) = bv;
