@@ -3,9 +3,10 @@
 //
 // With rows p of expert e = the e-th run of d_offsets, all sums in fp32 on
 // v_mfma_f32_16x16x32_bf16:
-//   k_rows_mm<NT>   y[p][n]  = sum_k x[src(p)][k] W[e][n][k]
-//   k_rows_mm<NN>   dx[p][k] = sum_n dy[p][n] W[e][n][k]   (and a second pair)
-//   k_wgrad         dW[e][n][k] = sum_{p in e} dy[p][n] x[src(p)][k]
+//   k_rows_mm<kNT>      y[p][n]  = sum_k x[src(p)][k] W[e][n][k]
+//   k_rows_mm<kGateUp>  the same with gate and up, h = silu(a) b
+//   k_rows_mm<kNN>      dx[p][k] = sum_n dy[p][n] W[e][n][k]   (and a second pair)
+//   k_wgrad             dW[e][n][k] = sum_{p in e} dy[p][n] x[src(p)][k]
 //
 // An operand's tile of one stage (64 steps of the reduction) goes from memory
 // straight to LDS (buffer loads with the LDS as destination: 16 bytes a lane,
@@ -18,8 +19,19 @@
 //     read through the LDS transpose load (4 x 16 blocks); 32-byte chunk c of
 //     row r sits at chunk c ^ (r & 3 | r >> 1 & 4), so the eight rows that
 //     half a wave reads hit eight different 32-byte bank groups.
-// The output position that is contiguous in memory is the A operand of the
-// MFMA: a lane then holds four neighbouring outputs of one row.
+// Counters show no bank conflict for either.  The output position that is
+// contiguous in memory is the A operand of the MFMA: a lane then holds four
+// neighbouring outputs of one row.
+//
+// What bounds it.  Tiles of 256 x 256 on eight waves read 12 fragments (12 KB)
+// from LDS per 32 MFMAs and wave, 96 of the 128 bytes a clock that LDS gives,
+// and 64 KB from L2 per stage and CU.  8192^3: 1150-1200 TFLOP/s forward,
+// 1200-1280 input gradient, 1080-1170 weight gradient, 1300-1400 gate/up,
+// against 1340-1400 of the library's product on the same boxes; zeros run
+// faster, so the clock under load is part of that.  With about 256 rows an
+// expert the weights' stream from HBM (one 32 KB stage a CU per 1.5 us with all
+// CUs) and the matrix units (1.2 us) take turns being the limit; with few rows
+// it is HBM alone (64 experts, 32 tokens: 6.2 TB/s).
 #include "device_common.h"
 #include "expert_rows.h"
 #include "internal.h"
@@ -431,7 +443,7 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
     constexpr int kPairs = GU ? 1 : 2;
     // The saved a and b: those of kAhead subtiles requested at once, in the
     // registers that the fragments leave (one at a time, each behind the
-    // stores before it, 32 experts of 255 rows took FIG us more).
+    // stores before it, 640 tiles of one stage took 112 us against 100).
     constexpr bool kGrad = FORM == kNN && EPI == kSwiglu;
     constexpr int kAhead = U > 8 ? 3 : 4;
     uint4 asave[kGrad ? kAhead : 1][kPairs], bsave[kGrad ? kAhead : 1][kPairs];
