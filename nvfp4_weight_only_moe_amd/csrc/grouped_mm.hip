@@ -42,6 +42,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 512;             // 8 waves: 2 along the rows x 4 along the columns
+constexpr int kWaves = kThreads / kWave;
 constexpr int kBN = 256;                  // output columns per tile, 64 per wave
 constexpr int kNI = 4;                    // 16-column subtiles per wave
 constexpr int kBK = 64;                   // reduction steps per stage
@@ -248,13 +249,11 @@ __device__ __forceinline__ RowTile find_tile(const MmParams& P, int bid) {
 
 // ---- fragments: lane l holds output position l & 15, reduction steps
 // 8 (l >> 4) .. + 7 of the k-step
-template <int BK>                           // reduction steps of an LDS row
 __device__ __forceinline__ bf16x8 frag_rc(const lds_u8* tile, int lane_off, int sub) {
-    return *reinterpret_cast<const __attribute__((address_space(3))) bf16x8*>(tile + lane_off + sub * (BK * 32));
+    return *reinterpret_cast<const __attribute__((address_space(3))) bf16x8*>(tile + lane_off + sub * (16 * kBK * 2));
 }
-// LDS unit (16 bytes) of unit u of row r
-template <int BK>
-__device__ __forceinline__ int rc_swizzle(int r) { return BK == 64 ? (r >> 1) & 7 : (r >> 2) & 3; }
+// LDS unit (16 bytes) of unit u of row r: u ^ rc_swizzle(r)
+__device__ __forceinline__ int rc_swizzle(int r) { return (r >> 1) & 7; }
 template <int ROW>                          // bytes of an LDS row
 __device__ __forceinline__ bf16x8 frag_ro(const lds_u8* tile, int lane_off) {
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + lane_off));
@@ -302,18 +301,16 @@ __device__ __forceinline__ floatx4 widen4(uint32_t lo, uint32_t hi) {
                    __uint_as_float(hi & 0xFFFF0000u)};
 }
 
-constexpr int rows_lds(int BM, int BK, int NSA, int NSB) { return (NSA * BM + NSB * kBN) * BK * 2; }
+constexpr int rows_lds(int BM, int NSA, int NSB) { return (NSA * BM + NSB * kBN) * kBK * 2; }
 
-// One tile of up to BM rows by 256 columns on W waves, W / 4 along the rows by
-// 4 along the columns, in stages of BK reduction steps: U 16-row subtiles a
-// wave.  The two waves of a SIMD (W == 8) take the tile's subtiles in turn, so
-// a short tile costs both the same.
-template <int FORM, int EPI, int W, int BM, int U, int BK, int NSA, int NSB>
+// One tile of up to BM rows by 256 columns on eight waves, two along the rows
+// by four along the columns: U 16-row subtiles a wave.  The two waves of a
+// SIMD take the tile's subtiles in turn, so a short tile costs both the same.
+template <int FORM, int EPI, int BM, int U, int NSA, int NSB>
 __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, uint8_t* smem) {
-    constexpr int WM = W / 4;
-    constexpr int kRowBytes = BM * BK * 2, kColStage = kBN * BK * 2, kColRing = NSA * kRowBytes;
-    constexpr int kADma = kRowBytes / 1024 / W, kBDma = kColStage / 1024 / W;
-    constexpr int kDmaRows = 512 / BK, kUnits = BK / 8;       // rows of a DMA, 16-byte units of a row (RC)
+    constexpr int kRowBytes = BM * kBK * 2, kColStage = kBN * kBK * 2, kColRing = NSA * kRowBytes;
+    constexpr int kADma = kRowBytes / 1024 / kWaves, kBDma = kColStage / 1024 / kWaves;
+    constexpr int kDmaRows = 512 / kBK, kUnits = kBK / 8;       // rows of a DMA, 16-byte units of a row (RC)
     constexpr bool RC = FORM != kNN, GU = FORM == kGateUp;    // GU: 128 gate + 128 up columns per tile
     constexpr int kTileCols = GU ? kBN / 2 : kBN;             // output columns per tile
     const int lane = threadIdx.x & 63;
@@ -323,20 +320,25 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
     const int c0 = t.ct * kTileCols;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_u8*)smem;
 
-    // row operand: per-lane byte offset of its rows (one per DMA)
+    // row operand: per-lane byte offset of its rows (one per DMA); all slots are
+    // asked for at once
     uint32_t aoff[kADma];
-    int aunit[kADma];
+    int aunit[kADma], slot[kADma];
     const int64_t abase = P.slots ? 0 : (int64_t)t.p0 * P.R;
+    const auto row = [&](int i) { return (i * kWaves + wave) * kDmaRows + lane / kUnits; };
+    if (P.slots) {
+#pragma unroll
+        for (int i = 0; i < kADma; ++i) slot[i] = P.slots[t.p0 + min(row(i), t.rows - 1)];
+    }
 #pragma unroll
     for (int i = 0; i < kADma; ++i) {
-        const int r = (i * W + wave) * kDmaRows + lane / kUnits;
-        aunit[i] = (lane % kUnits) ^ rc_swizzle<BK>(r);
+        const int r = row(i);
+        aunit[i] = (lane % kUnits) ^ rc_swizzle(r);
         int src = r;
         bool ok = r < t.rows;
-        if (P.slots && ok) {
-            const int slot = P.slots[t.p0 + r];
-            src = slot_token(slot, P.k, P.kmagic);
-            ok = slot >= 0 && src < P.X;
+        if (P.slots) {
+            src = slot_token(slot[i], P.k, P.kmagic);
+            ok = ok && slot[i] >= 0 && src < P.X;
         }
         aoff[i] = ok ? (uint32_t)src * (uint32_t)P.R * 2u + aunit[i] * 16 : kOutside;
     }
@@ -347,54 +349,54 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
 #pragma unroll
     for (int i = 0; i < kBDma; ++i) {
         if constexpr (RC) {
-            const int r = (i * W + wave) * kDmaRows + lane / kUnits;
+            const int r = (i * kWaves + wave) * kDmaRows + lane / kUnits;
             const int n = GU ? r & (kBN / 2 - 1) : r;
-            bpos[i] = (lane % kUnits) ^ rc_swizzle<BK>(r);
+            bpos[i] = (lane % kUnits) ^ rc_swizzle(r);
             boff[i] = c0 + n < P.C ? (uint32_t)n * (uint32_t)P.R * 2u + bpos[i] * 16 : kOutside;
         } else {
-            const int r = (i * W + wave) * 2 + (lane >> 5);
+            const int r = (i * kWaves + wave) * 2 + (lane >> 5);
             const int pos = lane & 31, col = (((pos >> 1) ^ ro_swizzle(r)) << 4) + ((pos & 1) << 3);
             bpos[i] = r;
             boff[i] = c0 + col < P.C ? (uint32_t)r * (uint32_t)P.C * 2u + col * 2 : kOutside;
         }
     }
 
-    const int spp = (P.R + BK - 1) / BK;            // stages per pair
+    const int spp = (P.R + kBK - 1) / kBK;            // stages per pair
     const int all = spp * P.pairs;
     const int first = EPI == kPart ? (int)((int64_t)all * t.slice / P.slices) : 0;
     const int nstages = (EPI == kPart ? (int)((int64_t)all * (t.slice + 1) / P.slices) : all) - first;
     const auto dma_a = [&](int s) {
         const int pair = FORM == kNN && first + s >= spp ? 1 : 0;
-        const int r0 = (first + s - pair * spp) * BK;
+        const int r0 = (first + s - pair * spp) * kBK;
         const uint16_t* a = uniform_ptr((pair ? P.a1 : P.a0) + abase + r0);
         const uint32_t buf = lds0 + (s % NSA) * kRowBytes;
 #pragma unroll
         for (int i = 0; i < kADma; ++i) {
             const uint32_t vo = r0 + aunit[i] * 8 < P.R ? aoff[i] : kOutside;
-            lds_dma16_buf(a, vo, buf + (i * W + wave) * 1024);
+            lds_dma16_buf(a, vo, buf + (i * kWaves + wave) * 1024);
         }
     };
     const auto dma_b = [&](int s) {
         const int pair = FORM == kNN && first + s >= spp ? 1 : 0;
-        const int r0 = (first + s - pair * spp) * BK;
+        const int r0 = (first + s - pair * spp) * kBK;
         const uint32_t buf = lds0 + kColRing + (s % NSB) * kColStage;
 #pragma unroll
         for (int i = 0; i < kBDma; ++i) {
             const bool up = GU && i >= kBDma / 2;
             const uint16_t* w = uniform_ptr((pair || up ? P.w1 : P.w0) + wbase + (RC ? (int64_t)r0 : (int64_t)r0 * P.C));
             const bool ok = RC ? r0 + bpos[i] * 8 < P.R : r0 + bpos[i] < P.R;
-            lds_dma16_buf(w, ok ? boff[i] : kOutside, buf + (i * W + wave) * 1024);
+            lds_dma16_buf(w, ok ? boff[i] : kOutside, buf + (i * kWaves + wave) * 1024);
         }
     };
 
     // lane offsets of the fragments
-    int aread[BK / 32], bread[BK / 32], bchunk[kNI];
+    int aread[kBK / 32], bread[kBK / 32], bchunk[kNI];
 #pragma unroll
-    for (int ks = 0; ks < BK / 32; ++ks) {
-        const int u = ((ks * 4 + q) ^ rc_swizzle<BK>(lrow)) * 16;
-        aread[ks] = (wm * 16 + lrow) * BK * 2 + u;
+    for (int ks = 0; ks < kBK / 32; ++ks) {
+        const int u = ((ks * 4 + q) ^ rc_swizzle(lrow)) * 16;
+        aread[ks] = (wm * 16 + lrow) * kBK * 2 + u;
         if constexpr (RC)
-            bread[ks] = ((GU ? wn * 32 : wn * 64) + lrow) * BK * 2 + u;
+            bread[ks] = ((GU ? wn * 32 : wn * 64) + lrow) * kBK * 2 + u;
         else
             bread[ks] = (ks * 32 + q * 8 + (lrow >> 2)) * 512 + (lrow & 3) * 8;
     }
@@ -408,32 +410,27 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
 #pragma unroll
         for (int ni = 0; ni < kNI; ++ni) acc[mi][ni] = floatx4{0, 0, 0, 0};
     const auto read_a = [&](int buf, int ks, int mi) {
-        return frag_rc<BK>((const lds_u8*)smem + buf * kRowBytes, aread[ks], WM * mi);
+        return frag_rc((const lds_u8*)smem + buf * kRowBytes, aread[ks], 2 * mi);
     };
     const auto read_b = [&](int buf, int ks, int ni) {
         const lds_u8* bs = (const lds_u8*)smem + kColRing + buf * kColStage;
-        if constexpr (RC) return frag_rc<BK>(bs, bread[ks], GU && ni >= 2 ? ni + 6 : ni);
+        if constexpr (RC) return frag_rc(bs, bread[ks], GU && ni >= 2 ? ni + 6 : ni);
         else return frag_ro<512>(bs, bread[ks] + bchunk[ni]);
     };
     constexpr int kReadsB = RC ? 1 : 2;
-    if constexpr (BK == 64)
-        run_stages<NSA, NSB, U, kNI, kADma, kBDma, 1, kReadsB>(nstages, dma_a, dma_b, read_a, read_b, acc);
-    else
-        run_steps<NSA, U, kNI, kADma + kBDma, 1, kReadsB>(
-            nstages, [&](int s) { dma_a(s); dma_b(s); }, [&](int buf, int mi) { return read_a(buf, 0, mi); },
-            [&](int buf, int ni) { return read_b(buf, 0, ni); }, acc);
+    run_stages<NSA, NSB, U, kNI, kADma, kBDma, 1, kReadsB>(nstages, dma_a, dma_b, read_a, read_b, acc);
 
     if constexpr (EPI == kPart) {
 #pragma unroll
         for (int mi = 0; mi < U; ++mi) {
-            const int r = (mi * WM + wm) * 16 + lrow;
+            const int r = (mi * 2 + wm) * 16 + lrow;
             if (r >= t.rows) continue;
 #pragma unroll
             for (int ni = 0; ni < kNI; ++ni) {
                 const int up = GU && ni >= 2 ? 1 : 0, c = c0 + (GU ? wn * 32 + ni % 2 * 16 : wn * 64 + ni * 16) + q * 4;
                 if (c >= P.C) continue;
-                const int64_t row = ((int64_t)(t.slice * (GU ? 2 : 1) + up) * P.M + t.p0 + r) * P.C;
-                *reinterpret_cast<floatx4*>(P.part + row + c) = acc[mi][ni];
+                const int64_t at = ((int64_t)(t.slice * (GU ? 2 : 1) + up) * P.M + t.p0 + r) * P.C + c;
+                *reinterpret_cast<floatx4*>(P.part + at) = acc[mi][ni];
             }
         }
         return;
@@ -449,7 +446,7 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
     uint4 asave[kGrad ? kAhead : 1][kPairs], bsave[kGrad ? kAhead : 1][kPairs];
 #pragma unroll
     for (int mi = 0; mi < U; ++mi) {
-        const int r = (mi * WM + wm) * 16 + lrow;
+        const int r = (mi * 2 + wm) * 16 + lrow;
         if constexpr (kGrad) {
             if (mi % kAhead == 0)
 #pragma unroll
@@ -458,7 +455,7 @@ __device__ __forceinline__ void rows_tile(const MmParams& P, const RowTile& t, u
                     for (int j = 0; j < kPairs; ++j) {
                         // lanes outside read the tile's last row or columns, so
                         // that no load waits behind a branch
-                        const int ra = min(((mi + i) * WM + wm) * 16 + lrow, t.rows - 1);
+                        const int ra = min(((mi + i) * 2 + wm) * 16 + lrow, t.rows - 1);
                         const int ca = min(c0 + wn * 64 + j * 32 + (q & 1) * 16 + (q >> 1) * 8, P.C - 8);
                         const int64_t at = (int64_t)(t.p0 + ra) * P.C + ca;
                         asave[i][j] = *reinterpret_cast<const uint4*>(P.i0 + at);
@@ -521,15 +518,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_rows_mm(MmParams P) {
     extern __shared__ __align__(16) uint8_t smem[];
     const RowTile t = find_tile<BM, EPI == kPart>(P, blockIdx.x);
     if (t.e < 0) return;
-    if (t.rows <= 32) rows_tile<FORM, EPI, 8, 64, 1, 64, 4, 4>(P, t, smem);
-    else if (BM == 64 || t.rows <= 64) rows_tile<FORM, EPI, 8, 64, 2, 64, 4, 4>(P, t, smem);
+    if (t.rows <= 32) rows_tile<FORM, EPI, 64, 1, 4, 4>(P, t, smem);
+    else if (BM == 64 || t.rows <= 64) rows_tile<FORM, EPI, 64, 2, 4, 4>(P, t, smem);
     else if constexpr (BM > 64) {
-        if (t.rows <= 96) rows_tile<FORM, EPI, 8, 128, 3, 64, 3, 3>(P, t, smem);
-        else if (t.rows <= 128) rows_tile<FORM, EPI, 8, 128, 4, 64, 3, 3>(P, t, smem);
-        else if (t.rows <= 160) rows_tile<FORM, EPI, 8, 192, 5, 64, 2, 3>(P, t, smem);
-        else if (t.rows <= 192) rows_tile<FORM, EPI, 8, 192, 6, 64, 2, 3>(P, t, smem);
-        else if (t.rows <= 256) rows_tile<FORM, EPI, 8, 256, 8, 64, 2, 3>(P, t, smem);
-        else rows_tile<FORM, EPI, 8, 320, 9, 64, 2, 2>(P, t, smem);
+        if (t.rows <= 96) rows_tile<FORM, EPI, 128, 3, 3, 3>(P, t, smem);
+        else if (t.rows <= 128) rows_tile<FORM, EPI, 128, 4, 3, 3>(P, t, smem);
+        else if (t.rows <= 160) rows_tile<FORM, EPI, 192, 5, 2, 3>(P, t, smem);
+        else if (t.rows <= 192) rows_tile<FORM, EPI, 192, 6, 2, 3>(P, t, smem);
+        else if (t.rows <= 256) rows_tile<FORM, EPI, 256, 8, 2, 3>(P, t, smem);
+        else rows_tile<FORM, EPI, 320, 9, 2, 2>(P, t, smem);
     }
 }
 
@@ -818,8 +815,8 @@ RowsPlan rows_plan(int M, int E, int R, int C, int pairs, int outs, int ntc) {
 template <int FORM, int EPI, int BM>
 moe_status launch_rows(const MmParams& P, const char* name, hipStream_t s) {
     const int64_t grid = xcd_grid(row_tiles_bound(P.M, P.E, BM) * P.ntc * (EPI == kPart ? P.slices : 1));
-    constexpr size_t lds = rows_lds(256, 64, 2, 3);
-    static_assert(rows_lds(64, 64, 4, 4) <= lds && rows_lds(128, 64, 3, 3) <= lds && rows_lds(320, 64, 2, 2) <= lds,
+    constexpr size_t lds = rows_lds(256, 2, 3);
+    static_assert(rows_lds(64, 4, 4) <= lds && rows_lds(128, 3, 3) <= lds && rows_lds(320, 2, 2) <= lds,
                   "one size");
     moe_status st = allow_dynamic_lds(reinterpret_cast<const void*>(&k_rows_mm<FORM, EPI, BM>), lds);
     if (st != MOE_OK) return st;
