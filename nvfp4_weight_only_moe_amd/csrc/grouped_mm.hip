@@ -525,6 +525,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_rows_mm(MmParams P) {
         else if (t.rows <= 128) rows_tile<FORM, EPI, 128, 4, 3, 3>(P, t, smem);
         else if (t.rows <= 160) rows_tile<FORM, EPI, 192, 5, 2, 3>(P, t, smem);
         else if (t.rows <= 192) rows_tile<FORM, EPI, 192, 6, 2, 3>(P, t, smem);
+        else if (t.rows <= 224) rows_tile<FORM, EPI, 256, 7, 2, 3>(P, t, smem);
         else if (t.rows <= 256) rows_tile<FORM, EPI, 256, 8, 2, 3>(P, t, smem);
         else rows_tile<FORM, EPI, 320, 9, 2, 2>(P, t, smem);
     }
@@ -597,20 +598,24 @@ struct WgradParams {
 
 constexpr int kSrcRows = 1024;    // gathered rows whose places in x are kept in LDS at a time
 
-constexpr int wgrad_lds(int W, int MI, int NI, int BK, int NS) {
-    return NS * (MI * (W / 4) * 16 + NI * 64) * BK * 2 + kSrcRows * 4;
+constexpr int wgrad_lds(int WM, int WN, int MI, int NI, int BK, int NSA, int NSB) {
+    return (NSA * MI * WM * 16 + NSB * NI * WN * 16) * BK * 2 + (NSA == NSB ? kSrcRows * 4 : 0);
 }
 
-// One workgroup of W waves, W / 4 along n by 4 along k: a tile of 4 W MI x
-// 64 NI of one expert's dW over one slice of its rows, in stages of BK rows.
-template <int W, int MI, int NI, int BK, int NS>
-__global__ void __launch_bounds__(W * kWave, 2) k_wgrad(WgradParams P) {
-    constexpr int TM = W / 4 * MI * 16, TN = NI * 64;               // rows n, columns k of the tile
-    constexpr int kABytes = TM * BK * 2, kBBytes = TN * BK * 2, kStageBytes = kABytes + kBBytes;
+// One workgroup of WM waves along n by WN along k: a tile of 16 WM MI x 16 WN
+// NI of one expert's dW over one slice of its rows, in stages of BK rows,
+// NSA of dy's and NSB of x's in LDS (NSB > NSA: nothing is gathered, and the
+// table of gathered rows has no room; x, the wider one, is then a stage more
+// ahead).
+template <int WM, int WN, int MI, int NI, int BK, int NSA, int NSB>
+__global__ void __launch_bounds__(WM * WN * kWave, 2) k_wgrad(WgradParams P) {
+    constexpr int W = WM * WN, TM = WM * MI * 16, TN = WN * NI * 16;   // waves; rows n, columns k of the tile
+    constexpr int kABytes = TM * BK * 2, kBBytes = TN * BK * 2, kBRing = NSA * kABytes;
     constexpr int kADma = kABytes / 1024 / W, kBDma = kBBytes / 1024 / W;
     constexpr int kARows = 512 / TM, kBRows = 512 / TN;             // LDS rows per DMA
     extern __shared__ __align__(16) uint8_t smem[];
-    uint32_t* srcs = reinterpret_cast<uint32_t*>(smem + NS * kStageBytes);
+    uint32_t* srcs = reinterpret_cast<uint32_t*>(smem + kBRing + NSB * kBBytes);
+    constexpr bool kGather = NSA == NSB;
     const int per = P.ntn * P.ntk;
     const Piece f = find_piece<true>(P.offsets, P.E, P.M, P.slice, per, blockIdx.x);
     if (f.e < 0) return;
@@ -619,7 +624,7 @@ __global__ void __launch_bounds__(W * kWave, 2) k_wgrad(WgradParams P) {
     const int p0 = f.lo + sl * P.slice, cnt = min(f.n - sl * P.slice, P.slice);
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave >> 2, wn = wave & 3;
+    const int wm = wave / WN, wn = wave % WN;
     const int lrow = lane & 15, q = lane >> 4;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_u8*)smem;
 
@@ -652,7 +657,7 @@ __global__ void __launch_bounds__(W * kWave, 2) k_wgrad(WgradParams P) {
     };
     const auto dma_a = [&](int s) {
         const int r0 = s * BK;
-        const uint32_t buf = lds0 + (s % NS) * kStageBytes;
+        const uint32_t buf = lds0 + (s % NSA) * kABytes;
         const uint16_t* a = uniform_ptr(P.dy + (int64_t)(p0 + r0) * P.N + n0);
 #pragma unroll
         for (int i = 0; i < kADma; ++i)
@@ -660,15 +665,15 @@ __global__ void __launch_bounds__(W * kWave, 2) k_wgrad(WgradParams P) {
     };
     const auto dma_b = [&](int s) {
         const int r0 = s * BK;
-        const uint32_t buf = lds0 + (s % NS) * kStageBytes;
-        if (P.slots && r0 % kSrcRows == 0) look_up(s);
-        const uint16_t* x = uniform_ptr(P.x + (P.slots ? 0 : (int64_t)(p0 + r0) * P.K) + k0);
+        const uint32_t buf = lds0 + kBRing + (s % NSB) * kBBytes;
+        if (kGather && P.slots && r0 % kSrcRows == 0) look_up(s);
+        const uint16_t* x = uniform_ptr(P.x + (kGather && P.slots ? 0 : (int64_t)(p0 + r0) * P.K) + k0);
 #pragma unroll
         for (int i = 0; i < kBDma; ++i) {
-            const uint32_t row = P.slots ? srcs[(r0 + xrow[i]) % kSrcRows]
+            const uint32_t row = kGather && P.slots ? srcs[(r0 + xrow[i]) % kSrcRows]
                                          : r0 + xrow[i] < cnt ? (uint32_t)xrow[i] * (uint32_t)P.K * 2u : kOutside;
             lds_dma16_buf(x, row != kOutside && xcol[i] != kOutside ? row + xcol[i] : kOutside,
-                          buf + kABytes + (i * W + wave) * 1024);
+                          buf + (i * W + wave) * 1024);
         }
     };
 
@@ -692,16 +697,16 @@ __global__ void __launch_bounds__(W * kWave, 2) k_wgrad(WgradParams P) {
         for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = floatx4{0, 0, 0, 0};
 
     const auto read_a = [&](int buf, int ks, int mi) {
-        return frag_ro<TM * 2>((const lds_u8*)smem + buf * kStageBytes, ard[ks] + ac[mi]);
+        return frag_ro<TM * 2>((const lds_u8*)smem + buf * kABytes, ard[ks] + ac[mi]);
     };
     const auto read_b = [&](int buf, int ks, int ni) {
-        return frag_ro<TN * 2>((const lds_u8*)smem + buf * kStageBytes + kABytes, brd[ks] + bc[ni]);
+        return frag_ro<TN * 2>((const lds_u8*)smem + kBRing + buf * kBBytes, brd[ks] + bc[ni]);
     };
     if (nstages > 0) {
         if constexpr (BK == 64)
-            run_stages<NS, NS, MI, NI, kADma, kBDma, 2, 2>(nstages, dma_a, dma_b, read_a, read_b, acc);
+            run_stages<NSA, NSB, MI, NI, kADma, kBDma, 2, 2>(nstages, dma_a, dma_b, read_a, read_b, acc);
         else
-            run_steps<NS, MI, NI, kADma + kBDma, 2, 2>(
+            run_steps<NSA, MI, NI, kADma + kBDma, 2, 2>(
                 nstages, [&](int s) { dma_a(s); dma_b(s); }, [&](int buf, int mi) { return read_a(buf, 0, mi); },
                 [&](int buf, int ni) { return read_b(buf, 0, ni); }, acc);
     }
@@ -841,29 +846,35 @@ moe_status launch_rows_any(MmParams P, const char* name, void* ws, hipStream_t s
 
 int column_tiles(int C, bool gate_up) { return gate_up ? (C + kBN / 2 - 1) / (kBN / 2) : (C + kBN - 1) / kBN; }
 
-// Tile of a weight gradient and rows of a slice of its reduction.
+// Tile of a weight gradient (rows n, columns k) and rows of a slice of its reduction.
 struct WgradPlan {
-    bool big;
-    int ntn, ntk, slice, parts;
+    int tn, tk, ntn, ntk, slice, parts;
     int64_t tiles, part_bytes;
 };
 
 WgradPlan wgrad_plan(int M, int N, int K, int E) {
     WgradPlan p{};
-    p.ntk = (K + 255) / 256;
+    const auto tile = [&](int tn, int tk) {
+        p.tn = tn;
+        p.tk = tk;
+        p.ntn = (N + tn - 1) / tn;
+        p.ntk = (K + tk - 1) / tk;
+        return (int64_t)p.ntn * p.ntk;
+    };
     // the tile of 256 n reads x half as often; the one of 128 leaves room for
     // two workgroups a CU, better with few rows (32 experts, 1536 x 5120: 16
     // rows 193 us against 206, 256 rows 321 against 310), and wastes less on a small N
-    p.big = M / E >= 192 && (N + 127) / 128 % 2 == 0;
-    const int TM = p.big ? 256 : 128;
-    p.ntn = (N + TM - 1) / TM;
-    const int64_t per = (int64_t)p.ntn * p.ntk, slots = p.big ? 256 : 512;
+    const bool big = M / E >= 192 && (N + 127) / 128 % 2 == 0;
+    const int64_t slots = big ? 256 : 512;
+    int64_t per = tile(big ? 256 : 128, 256);
     p.slice = 1 << 30;
     // Few tiles: slices of at least 8 stages (the join and its partial sums
     // cost as much), so that their number comes near the workgroups that run
-    // at once.
+    // at once.  Of 256 x 128 tiles half as many slices do it, and their partial
+    // sums are half as many bytes (one group of 8195 rows, 256 x 5120: 45 -> 38 us).
     if (2 * per * E <= slots) {
-        const int64_t want = slots / per, stages = (M + kBK - 1) / kBK;
+        if (big) per = tile(256, 128);
+        const int64_t want = std::max<int64_t>(1, slots / per), stages = (M + kBK - 1) / kBK;
         const int64_t rows = std::max<int64_t>((stages + want - 1) / want, 8) * kBK;
         if (rows < M) p.slice = (int)rows;
     }
@@ -873,13 +884,13 @@ WgradPlan wgrad_plan(int M, int N, int K, int E) {
     return p;
 }
 
-template <int W, int MI, int NI, int BK, int NS>
+template <int WM, int WN, int MI, int NI, int BK, int NSA, int NSB>
 moe_status launch_wgrad(const WgradParams& P, int64_t tiles, hipStream_t s) {
-    constexpr size_t lds = wgrad_lds(W, MI, NI, BK, NS);
-    moe_status st = allow_dynamic_lds(reinterpret_cast<const void*>(&k_wgrad<W, MI, NI, BK, NS>), lds);
+    constexpr size_t lds = wgrad_lds(WM, WN, MI, NI, BK, NSA, NSB);
+    moe_status st = allow_dynamic_lds(reinterpret_cast<const void*>(&k_wgrad<WM, WN, MI, NI, BK, NSA, NSB>), lds);
     if (st != MOE_OK) return st;
-    MOE_LAUNCH("grouped_wgrad", (k_wgrad<W, MI, NI, BK, NS>), dim3((unsigned)xcd_grid(tiles)), dim3(W * kWave), lds, s,
-               P);
+    MOE_LAUNCH("grouped_wgrad", (k_wgrad<WM, WN, MI, NI, BK, NSA, NSB>), dim3((unsigned)xcd_grid(tiles)), dim3(WM * WN * kWave),
+               lds, s, P);
     return MOE_OK;
 }
 
@@ -950,7 +961,10 @@ moe_status launch_grouped_wgrad(const GroupedArgs& g, float* dw, bool accumulate
     P.dw = dw;
     P.part = static_cast<float*>(ws);
     P.parts = p.parts;
-    const moe_status st = p.big ? launch_wgrad<8, 8, 4, 64, 2>(P, p.tiles, s) : launch_wgrad<4, 8, 4, 32, 3>(P, p.tiles, s);
+    const moe_status st = p.tn == 128   ? launch_wgrad<1, 4, 8, 4, 32, 3, 3>(P, p.tiles, s)
+                          : p.tk == 128 ? launch_wgrad<4, 2, 4, 4, 64, 3, 3>(P, p.tiles, s)
+                          : P.slots     ? launch_wgrad<2, 4, 8, 4, 64, 2, 2>(P, p.tiles, s)
+                                        : launch_wgrad<2, 4, 8, 4, 64, 2, 3>(P, p.tiles, s);
     if (st != MOE_OK || p.part_bytes == 0) return st;
     MOE_LAUNCH("grouped_wgrad_join", k_wgrad_join, dim3((unsigned)(((int64_t)g.N * g.K + 1023) / 1024), g.E), dim3(256),
                0, s, P);
