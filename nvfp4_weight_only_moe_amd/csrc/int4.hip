@@ -106,7 +106,7 @@ __device__ __forceinline__ uint4 order_x(uint4 v) {
 // groups' sums of it, the rings of weights.
 template <int RT, int TT>
 struct Int4Lds {
-    static constexpr int kUnits = TT == 1 ? 4 : 8;               // 16-byte units of x a thread brings per slab
+    static constexpr int kUnits = TT <= 2 ? 4 : 8;               // 16-byte units of x a thread brings per slab
     static constexpr int kX = kUnits * kIntThreads * 16 + 16 * TT * 16;      // rows are 16 bytes longer than a slab
     static constexpr int kSums = 4096, kRings = kIntWaves * kRing * RT * kSlot;
     static constexpr int kBytes = kX + kSums + kRings;
@@ -460,18 +460,39 @@ moe_status launch_int4(const Int4Params& P, hipStream_t s) {
     return P.zeros ? launch_int4_z<G, RT, TT, WR, true>(P, s) : launch_int4_z<G, RT, TT, WR, false>(P, s);
 }
 
+// The tile.  A workgroup reads all of its rows of x for 16 RT WR weight rows,
+// so a wide tile saves cache traffic, and one that leaves CUs empty costs more
+// than it saves.  The widest that fills most of the CUs is taken.  Bounds where
+// the two sides were measured (us; group 128 with zero points; "experts": 64):
+//   64 rows against 32: a tile costs 5/3 (experts of 75 rows, 1536 x 5120: 251
+//     against 238, of 256 rows: 480 against 606).  Its LDS leaves one to a CU:
+//     320 of them take two turns (1024 rows, 5120 x 5120: 132 against 120).
+//   32 rows against 16 (5120 x 1536): experts of 12 rows 79 against 73, of 20
+//     rows 86 against 114.
+//   WR 8 against 4, half the waves along K (8 rows of x, top 8): 8192 x 768 45
+//     against 68, 4096 x 2048 49 against 60, 2048 x 4096 50 against 52 (group 32
+//     56 against 54), 1536 x 5120 44 against 41.
+//   too few: 16 rows, 160 of WR 2 13.2 against 320 of WR 1 15.6 (5120 x 5120);
+//     128 of WR 2 31 against 256 of WR 1 26 (4096 x 14336).
 template <int G>
 moe_status launch_int4_group(const Int4Params& P, hipStream_t s) {
-    const int64_t experts = P.offsets ? std::min(P.E, P.M) : 1, mean = P.M / experts;
-    const int64_t columns = std::max<int64_t>(experts, 1) * P.N;     // weight rows that are read
     if (!P.offsets && P.M == 1) return launch_int4_vec<1>(P, G, s);
     if (!P.offsets && P.M == 2) return launch_int4_vec<2>(P, G, s);
-    if (mean > 32) {
-        if (columns * ((mean + 63) / 64) >= 256 * 128) return launch_int4<G, 2, 4, 4>(P, s);
-        return launch_int4<G, 2, 4, 2>(P, s);
+    const int64_t experts = P.offsets ? std::max<int64_t>(std::min(P.E, P.M), 1) : 1, rows = P.M / experts;
+    const auto tiles = [&](int64_t tok, int64_t nr) {            // 0: half of the tile's weight rows do not exist
+        return 2 * (int64_t)P.N > nr ? experts * ((rows + tok - 1) / tok) * ((P.N + nr - 1) / nr) : 0;
+    };
+    if (5 * ((rows + 63) / 64) < 3 * ((rows + 31) / 32)) {
+        const int64_t t = tiles(64, 256), turns = (t + 255) / 256;
+        if (t >= 192 && 10 * t >= 7 * 256 * turns) return launch_int4<G, 2, 4, 8>(P, s);
     }
-    if (mean > 16) return launch_int4<G, 1, 2, 1>(P, s);
-    if (columns >= 8 * 1024) return launch_int4<G, 1, 1, 4>(P, s);
+    if (rows > (P.offsets ? 12 : 16)) {
+        if (tiles(32, 128) >= 192) return launch_int4<G, 1, 2, 8>(P, s);
+        if (tiles(32, 64) >= 192) return launch_int4<G, 1, 2, 4>(P, s);
+    }
+    if (P.K < 4096 && tiles(16, 128) >= 160) return launch_int4<G, 1, 1, 8>(P, s);
+    if (tiles(16, 64) >= 160) return launch_int4<G, 1, 1, 4>(P, s);
+    if (tiles(16, 32) >= 160) return launch_int4<G, 1, 1, 2>(P, s);
     return launch_int4<G, 1, 1, 1>(P, s);
 }
 

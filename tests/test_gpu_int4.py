@@ -117,6 +117,31 @@ def test_experts(counts, K, N, G, zeros, k):
     assert (out[:pad] == 5.0).all() and (out[M - pad:] == 5.0).all()
 
 
+@pytest.mark.parametrize("zeros,G", [(False, 32), (True, 64), (True, 128)])
+@pytest.mark.parametrize("counts,K,N", [([3, 0, 16, 5] * 10, 640, 500), ([3, 0, 17, 5] * 10, 256, 250),
+                                        ([3, 0, 16, 5] * 10, 4224, 130), ([3, 0, 16, 5] * 10, 384, 100),
+                                        ([20, 31, 33, 1] * 4, 640, 1500), ([20, 31, 33, 1] * 4, 1152, 750),
+                                        ([60, 65, 40, 1, 0, 100] * 4, 640, 2000)])
+def test_experts_wide_tiles(counts, K, N, G, zeros):
+    """Enough experts and columns for every width of a tile, none of them a multiple of it."""
+    g = torch.Generator(device=DEV).manual_seed(sum(counts) + K + N + G)
+    t = weights(g, len(counts), N, K, G, zeros)
+    M, k = sum(counts), 2
+    x = torch.randn((M // k + 1, K), generator=g, device=DEV).to(BF)
+    slots = torch.randint(0, x.shape[0] * k, (M,), generator=g, device=DEV, dtype=torch.int32)
+    slots[1] = -1
+    off = offsets_of(counts)
+    check(B.moe_int4_linear(x, t, off, slots, k), source_rows(x, slots, k, M), t, off, "wide")
+
+
+@pytest.mark.parametrize("T,K,N", [(1000, 640, 2900), (16, 128, 20500), (40, 384, 6300)])
+def test_dense_wide_tiles(T, K, N):
+    g = torch.Generator(device=DEV).manual_seed(T + K + N)
+    t = weights(g, 1, N, K, 128, True)
+    x = torch.randn((T, K), generator=g, device=DEV).to(BF)
+    check(B.moe_int4_linear(x, t), x.to(F64), t, offsets_of([T]), "dense wide")
+
+
 def test_large_common_offset_of_x():
     """Rows far from zero: the offset's sum is large against the result."""
     g = torch.Generator(device=DEV).manual_seed(3)
