@@ -77,7 +77,7 @@ struct Int4Params {
 };
 
 constexpr int kIntThreads = 512, kIntWaves = kIntThreads / kWave;
-constexpr int kRing = 4;          // chunks of a wave on their way
+constexpr int kRing = 4;          // chunks of a wave on their way, a power of two
 constexpr int kSlot = 1280;       // bytes of a chunk in the ring: 16 rows x 64 of codes, 64 words of scales and zeros
 
 __device__ __forceinline__ u32x4 transpose4(u32x4 v) {
@@ -89,13 +89,18 @@ __device__ __forceinline__ u32x4 transpose4(u32x4 v) {
     return u32x4{(uint32_t)c[0], (uint32_t)c[1], (uint32_t)d[0], (uint32_t)d[1]};
 }
 
-// 128 + code of the 8 codes of a word, in the order k0 k4 k1 k5 k2 k6 k3 k7
-__device__ __forceinline__ bf16x8 codes_bf16(uint32_t w) {
-    u32x4 r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-    return __builtin_bit_cast(bf16x8, r);
-}
+// 128 + code, two codes of a word at a time.  The constants sit in vector
+// registers, so that the AND-OR is one instruction: it has room for one
+// constant of another kind, and with both the compiler splits it.
+struct Codes128 {
+    uint32_t low4 = 0x000F000Fu, base = 0x43004300u;
+    __device__ __forceinline__ Codes128() { asm("" : "+v"(low4), "+v"(base)); }
+    __device__ __forceinline__ uint32_t pair(uint32_t w, int i) const { return ((w >> (4 * i)) & low4) | base; }
+    // the 8 codes of a word, in the order k0 k4 k1 k5 k2 k6 k3 k7
+    __device__ __forceinline__ bf16x8 word(uint32_t w) const {
+        return __builtin_bit_cast(bf16x8, u32x4{pair(w, 0), pair(w, 1), pair(w, 2), pair(w, 3)});
+    }
+};
 // eight bf16 in that order
 __device__ __forceinline__ uint4 order_x(uint4 v) {
     return make_uint4(__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
@@ -222,7 +227,7 @@ __global__ void __launch_bounds__(kIntThreads, TT > 1 ? 2 : 4) k_int4_mm(Int4Par
     }
     const auto issue = [&](int i) {
         const int64_t cc = wk + i * WK;
-        const uint32_t slot = ring0 + (i % kRing) * (RT * kSlot);
+        const uint32_t slot = ring0 + (i & (kRing - 1)) * (RT * kSlot);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             lds_dma16(wbase[r] + cc * 64, (lds_void*)(uintptr_t)(slot + r * kSlot));
@@ -236,6 +241,7 @@ __global__ void __launch_bounds__(kIntThreads, TT > 1 ? 2 : 4) k_int4_mm(Int4Par
 #pragma unroll 1
     for (int i = 0; i < min(mine, kRing); ++i) issue(i);
 
+    const Codes128 decode;
     const floatx4 zero4 = {0, 0, 0, 0};
     floatx4 acc[RT][TT];
 #pragma unroll
@@ -258,7 +264,7 @@ __global__ void __launch_bounds__(kIntThreads, TT > 1 ? 2 : 4) k_int4_mm(Int4Par
             // the oldest chunk is in LDS
             if (mine - done >= kRing) wait_vmem_at_most<(kRing - 1) * RT * 2>();
             else wait_vmem_at_most<0>();
-            const uint8_t* slot = ring + (done % kRing) * (RT * kSlot);
+            const uint8_t* slot = ring + (done & (kRing - 1)) * (RT * kSlot);
             const int base = (c - first) * 128;
             u32x4 w[RT];
             uint32_t sc[RT][GC > 1 ? GC / 2 : 1], zp[RT];
@@ -282,7 +288,7 @@ __global__ void __launch_bounds__(kIntThreads, TT > 1 ? 2 : 4) k_int4_mm(Int4Par
                 const int g = ks / kSteps, kb = (base + (G == 128 ? q * 32 + ks * 8 : ks * 32 + q * 8)) * 2;
                 bf16x8 wf[RT];
 #pragma unroll
-                for (int r = 0; r < RT; ++r) wf[r] = codes_bf16(w[r][ks]);
+                for (int r = 0; r < RT; ++r) wf[r] = decode.word(w[r][ks]);
 #pragma unroll
                 for (int t = 0; t < TT; ++t) {
                     const bf16x8 xf = *reinterpret_cast<const bf16x8*>(smem + xrow[t] + kb);
@@ -356,6 +362,7 @@ __global__ void __launch_bounds__(kVecWaves * kWave, 4) k_int4_vec(Int4Params P,
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5, waves = blockDim.x >> 6, n0 = blockIdx.x * kVecRows;
     const int gshift = __builtin_ctz(G), groups = P.K >> gshift;
+    const Codes128 decode;
     float acc[kVecRows / 2][T];
 #pragma unroll
     for (int r = 0; r < kVecRows / 2; ++r)
@@ -404,7 +411,7 @@ __global__ void __launch_bounds__(kVecWaves * kWave, 4) k_int4_vec(Int4Params P,
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint32_t pair = ((cw[i] >> (4 * j)) & 0x000F000Fu) | 0x43004300u;
+                    const uint32_t pair = decode.pair(cw[i], j);
 #pragma unroll
                     for (int t = 0; t < T; ++t) {
                         const uint32_t xw = j == 0 ? xv[t][i].x : j == 1 ? xv[t][i].y : j == 2 ? xv[t][i].z : xv[t][i].w;
