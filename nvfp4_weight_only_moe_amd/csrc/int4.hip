@@ -78,7 +78,8 @@ struct Int4Params {
 
 constexpr int kIntThreads = 512, kIntWaves = kIntThreads / kWave;
 constexpr int kRing = 4;          // chunks of a wave on their way, a power of two
-constexpr int kSlot = 1280;       // bytes of a chunk in the ring: 16 rows x 64 of codes, 64 words of scales and zeros
+constexpr int kSlot = 1024;       // bytes of a chunk's codes: 16 rows x 64
+constexpr int kMeta = 256;        // a word per lane of scales and zero points
 
 __device__ __forceinline__ u32x4 transpose4(u32x4 v) {
     // word j of lane row i (16 lanes) -> word i of lane row j
@@ -109,11 +110,14 @@ __device__ __forceinline__ uint4 order_x(uint4 v) {
 
 // LDS of a workgroup against 16 TT rows of x: x (slab by slab of K), the
 // groups' sums of it, the rings of weights.
-template <int RT, int TT>
+template <int G, int RT, int TT, bool ZP>
 struct Int4Lds {
     static constexpr int kUnits = TT <= 2 ? 4 : 8;               // 16-byte units of x a thread brings per slab
     static constexpr int kX = kUnits * kIntThreads * 16 + 16 * TT * 16;      // rows are 16 bytes longer than a slab
-    static constexpr int kSums = 4096, kRings = kIntWaves * kRing * RT * kSlot;
+    static constexpr int kSums = 4096;
+    static constexpr int kMetas = G == 32 && ZP ? 2 : 1;         // words per lane of a pair of chunks
+    static constexpr int kCodes = kRing * RT * kSlot;            // of a wave, then its kRing / 2 pairs' words
+    static constexpr int kWave1 = kCodes + kRing / 2 * RT * kMetas * kMeta, kRings = kIntWaves * kWave1;
     static constexpr int kBytes = kX + kSums + kRings;
     static_assert(kIntWaves * RT * TT * 1024 <= kX + kSums + kRings, "the K parts meet in the same memory");
 };
@@ -123,8 +127,9 @@ struct Int4Lds {
 // chunks of 128 codes in turn; the K parts meet in LDS at the end.
 //
 // Weights: a wave's chunks run through a ring of its own in LDS, kRing deep,
-// by LDS-DMA (16 rows x 64 bytes, and a word per lane that holds the row's
-// scales or zero points), so that the loop over chunks stays rolled: unrolled
+// by LDS-DMA (16 rows x 64 bytes; the scales and zero points of two chunks in
+// a word per lane: with a word per lane and chunk, 64 experts, 1536 x 5120,
+// 8 rows of x, group 32: 50 us, 45 so), so that the loop over chunks stays rolled: unrolled
 // with its loads in registers its code is fetched as slowly as the weights
 // (one row of x, 5120 x 5120: 11.6 us).
 // x: a slab of its columns at a time, the next slab's loads issued before this
@@ -136,8 +141,8 @@ struct Int4Lds {
 template <int G, int RT, int TT, int WR, bool ZP>
 __global__ void __launch_bounds__(kIntThreads, TT > 1 ? 2 : 4) k_int4_mm(Int4Params P) {
     constexpr int WK = kIntWaves / WR, TOK = 16 * TT, GC = 128 / G, kNR = 16 * RT * WR;
-    using Lds = Int4Lds<RT, TT>;
-    constexpr int XU = Lds::kUnits;
+    using Lds = Int4Lds<G, RT, TT, ZP>;
+    constexpr int XU = Lds::kUnits, MI = Lds::kMetas;
     extern __shared__ __align__(16) uint8_t smem[];
     float* sums = reinterpret_cast<float*>(smem + Lds::kX);      // [group of the slab][stok]
 
@@ -213,33 +218,46 @@ __global__ void __launch_bounds__(kIntThreads, TT > 1 ? 2 : 4) k_int4_mm(Int4Par
     load_x(0);
 
     // weights: chunk i of the wave is chunk wk + i * WK of K
-    uint8_t* ring = smem + Lds::kX + Lds::kSums + wave * (kRing * RT * kSlot);
+    uint8_t* ring = smem + Lds::kX + Lds::kSums + wave * Lds::kWave1;
     const uint32_t ring0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)ring;
-    const uint8_t *wbase[RT], *mbase[RT];
+    const uint8_t* wbase[RT];
     int64_t moff[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
         const int64_t row = (int64_t)e * P.N + min(n0 + r * 16 + lrow, P.N - 1);
         wbase[r] = P.codes + row * (P.K / 2) + q * 16;
-        // words of the row's scales (lane rows 0, 1) and zero points (2), aligned down
         moff[r] = row * groups;
-        mbase[r] = ZP && q == 2 ? P.zeros : reinterpret_cast<const uint8_t*>(P.scales);
     }
-    const auto issue = [&](int i) {
-        const int64_t cc = wk + i * WK;
-        const uint32_t slot = ring0 + (i & (kRing - 1)) * (RT * kSlot);
+    const int mine = max((chunks - wk + WK - 1) / WK, 0), pairs = (mine + 1) / 2;      // the wave's chunks
+    // words of lane rows 0 .. 3: group 32: the two of a chunk's scales, then
+    // those of the pair's second chunk (zero points: in words of their own);
+    // else the pair's scales, then its zero points.  Aligned down to a word.
+    const auto issue_meta = [&](int pair) {
+        const uint32_t slot = ring0 + Lds::kCodes + (pair & (kRing / 2 - 1)) * (RT * MI * kMeta);
+        const auto group = [&](int r, int h) { return moff[r] + (int64_t)(wk + min(2 * pair + h, mine - 1) * WK) * GC; };
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-            lds_dma16(wbase[r] + cc * 64, (lds_void*)(uintptr_t)(slot + r * kSlot));
-            const int64_t g = moff[r] + cc * GC;
-            const int64_t at = ZP && q == 2 ? g & ~3ll : (g * 2 & ~3ll) + (GC == 4 && q == 1 ? 4 : 0);
-            lds_dma4(mbase[r] + at, (lds_void*)(uintptr_t)(slot + r * kSlot + 1024));
+            const uint8_t* at = reinterpret_cast<const uint8_t*>(P.scales);
+            if constexpr (G == 32) at += group(r, q >> 1) * 2 + (q & 1) * 4;
+            else if (ZP && q >= 2) at = P.zeros + (group(r, q & 1) & ~3ll);
+            else at += group(r, q & 1) * 2 & ~3ll;
+            lds_dma4(at, (lds_void*)(uintptr_t)(slot + r * MI * kMeta));
+            if constexpr (MI == 2) lds_dma4(P.zeros + group(r, q & 1), (lds_void*)(uintptr_t)(slot + r * MI * kMeta + kMeta));
         }
     };
-    const int mine = max((chunks - wk + WK - 1) / WK, 0);        // the wave's chunks
+    // chunk i; the second of a pair brings the pair's words
+    const auto issue = [&](int i) {
+        if (i & 1) issue_meta(i >> 1);
+        if (i < mine) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+                lds_dma16(wbase[r] + (int64_t)(wk + i * WK) * 64,
+                          (lds_void*)(uintptr_t)(ring0 + ((i & (kRing - 1)) * RT + r) * kSlot));
+        }
+    };
     int done = 0;
 #pragma unroll 1
-    for (int i = 0; i < min(mine, kRing); ++i) issue(i);
+    for (int i = 0; i < min(2 * pairs, kRing); ++i) issue(i);
 
     const Codes128 decode;
     const floatx4 zero4 = {0, 0, 0, 0};
@@ -261,21 +279,24 @@ __global__ void __launch_bounds__(kIntThreads, TT > 1 ? 2 : 4) k_int4_mm(Int4Par
         if (k0 + slab < P.K) load_x(k0 + slab);
 #pragma unroll 1
         for (int c = first + wk; c <= last; c += WK) {
-            // the oldest chunk is in LDS
-            if (mine - done >= kRing) wait_vmem_at_most<(kRing - 1) * RT * 2>();
+            // the oldest chunk and its pair's words are in LDS: of what was
+            // asked for later, three chunks and one pair's words are left
+            if (mine - done >= kRing) wait_vmem_at_most<(kRing - 1 + MI) * RT>();
             else wait_vmem_at_most<0>();
             const uint8_t* slot = ring + (done & (kRing - 1)) * (RT * kSlot);
-            const int base = (c - first) * 128;
+            const uint32_t* words = reinterpret_cast<const uint32_t*>(
+                ring + Lds::kCodes + ((done >> 1) & (kRing / 2 - 1)) * (RT * MI * kMeta)) + lrow;
+            const int base = (c - first) * 128, h = done & 1;
             u32x4 w[RT];
             uint32_t sc[RT][GC > 1 ? GC / 2 : 1], zp[RT];
             int odd[RT];
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
                 const uint4 v = *reinterpret_cast<const uint4*>(slot + r * kSlot + lane * 16);
-                const uint32_t* meta = reinterpret_cast<const uint32_t*>(slot + r * kSlot + 1024) + lrow;
-                sc[r][0] = meta[0];
-                if constexpr (GC == 4) sc[r][1] = meta[16];
-                if constexpr (ZP) zp[r] = meta[32];
+                const uint32_t* meta = words + r * MI * (kMeta / 4);
+                sc[r][0] = meta[(GC == 4 ? 2 * h : h) * 16];
+                if constexpr (GC == 4) sc[r][1] = meta[(2 * h + 1) * 16];
+                if constexpr (ZP) zp[r] = meta[GC == 4 ? 64 + h * 16 : 32 + h * 16];
                 odd[r] = GC == 4 ? 0 : (int)(moff[r] + c * GC) & 3;     // the first group inside its words
                 // with one group a chunk the order of K inside it is free:
                 // lane row q then takes codes 32 q .. + 31 as loaded
@@ -285,6 +306,9 @@ __global__ void __launch_bounds__(kIntThreads, TT > 1 ? 2 : 4) k_int4_mm(Int4Par
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
                 constexpr int kSteps = G / 32;                   // k-steps of a group
+                // the steps' loads together do not fit the registers (4096 rows,
+                // 5120 x 5120, zero points: 648 us, 530 so)
+                if (G == 32 && RT * TT == 8 && ks) __builtin_amdgcn_sched_barrier(0);
                 const int g = ks / kSteps, kb = (base + (G == 128 ? q * 32 + ks * 8 : ks * 32 + q * 8)) * 2;
                 bf16x8 wf[RT];
 #pragma unroll
@@ -318,7 +342,7 @@ __global__ void __launch_bounds__(kIntThreads, TT > 1 ? 2 : 4) k_int4_mm(Int4Par
                 }
             }
             __builtin_amdgcn_s_waitcnt(0xC07F);                  // lgkmcnt 0: the slot has been read
-            if (done + kRing < mine) issue(done + kRing);
+            if (done + kRing < 2 * pairs) issue(done + kRing);
             ++done;
         }
     }
@@ -455,7 +479,7 @@ moe_status launch_int4_z(Int4Params P, hipStream_t s) {
     P.ntn = (P.N + NR - 1) / NR;
     const int64_t blocks = P.offsets ? P.M / TOK + (int64_t)std::min(P.E, P.M) : (P.M + TOK - 1) / TOK;
     if (blocks * P.ntn >= (1 << 22)) return MOE_ERR_SHAPE;
-    const size_t lds = Int4Lds<RT, TT>::kBytes;
+    const size_t lds = Int4Lds<G, RT, TT, ZP>::kBytes;
     moe_status st = allow_dynamic_lds(reinterpret_cast<const void*>(&k_int4_mm<G, RT, TT, WR, ZP>), lds);
     if (st != MOE_OK) return st;
     MOE_LAUNCH("int4_linear", (k_int4_mm<G, RT, TT, WR, ZP>), dim3((unsigned)xcd_grid(blocks * P.ntn)),
