@@ -486,7 +486,8 @@ moe_status moe_int4_dequantize(const moe_int4_tensor *t, float *d_w_out, hipStre
  *   slots; given: rows by expert, with d_sorted_slots as in moe_grouped_linear.
  *   d_out bf16 [M][N].  Any N; M == 0 is a no-op; MOE_ERR_SHAPE from 2^22
  *   blocks of up to 64 rows by up to 256 columns.  The sums are formed as
- *   (128 + code) x less (128 + zero) x: an infinite x gives NaN.  Weights are
+ *   (128 + code) x less (128 + zero) x: an infinite x gives NaN, and so may
+ *   values from 2^113 on (a group's sum of 143 times them overflows).  Weights are
  *   streamed once per block of rows: the form for decode.  Deterministic;
  *   graph-capturable.
  */

@@ -542,22 +542,25 @@ def _entry(fn):
     """Runs an entry point on the device of its first tensor and on `stream`
     (default: that device's current stream): outputs and workspaces that the
     call allocates belong to the stream that the kernels run on."""
+    name = fn.__code__.co_varnames[0]
+
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
+        first = args[0] if args else kw.get(name)
         if not isinstance(first, (torch.Tensor, Int4Tensor)):
-            raise ValueError(f"{fn.__name__}: expected a torch.Tensor, got {type(first).__name__}")
+            raise ValueError(f"{fn.__name__}: {name}: expected a torch.Tensor, got {type(first).__name__}")
         dev = first.get_device()
         if dev < 0:
             raise ValueError(f"{fn.__name__}: expected a device (cuda) tensor, got {first.device}")
         if stream is None:
             if dev == _current_device():
-                return fn(first, *args, **kw)
+                return fn(*args, **kw)
             with torch.cuda.device(dev):
-                return fn(first, *args, **kw)
+                return fn(*args, **kw)
         if stream.device != first.device:
             raise ValueError(f"stream: on {stream.device}, the tensors are on {first.device}")
         with torch.cuda.stream(stream):
-            return fn(first, *args, **kw)
+            return fn(*args, **kw)
     return call
 
 

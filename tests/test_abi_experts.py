@@ -199,7 +199,8 @@ def test_binding_refuses_host_tensors_and_wrong_types():
                  lambda: b.moe_grouped_linear_wgrad(x, x, off), lambda: b.moe_combine(x, off, 1),
                  lambda: b.moe_int4_quantize_pack(w), lambda: b.moe_combine_backward(x, x, off, x),
                  lambda: b.moe_int4_linear(x, None), lambda: b.moe_int4_dequantize(None),
-                 lambda: b.moe_grouped_linear("x", w, off)):
+                 lambda: b.moe_grouped_linear("x", w, off), lambda: b.moe_grouped_linear(),
+                 lambda: b.moe_grouped_linear(w=w, x=x, offsets=off), lambda: b.moe_int4_linear(w=None, x=x)):
         with pytest.raises(ValueError):
             call()
 
