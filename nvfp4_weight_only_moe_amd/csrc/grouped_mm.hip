@@ -855,7 +855,7 @@ struct WgradPlan {
     int64_t tiles, part_bytes;
 };
 
-WgradPlan wgrad_plan(int M, int N, int K, int E) {
+WgradPlan wgrad_plan(int M, int N, int K, int E, bool gathered) {
     WgradPlan p{};
     const auto tile = [&](int tn, int tk) {
         p.tn = tn;
@@ -865,8 +865,11 @@ WgradPlan wgrad_plan(int M, int N, int K, int E) {
         return (int64_t)p.ntn * p.ntk;
     };
     // the tile of 256 n reads x half as often; the one of 128 leaves room for
-    // two workgroups a CU, better with few rows (32 experts, 1536 x 5120: 16
-    // rows 193 us against 206, 256 rows 321 against 310), and wastes less on a small N
+    // two workgroups a CU, one storing while the other multiplies, and wastes
+    // less on a small N (32 experts, 5120 x 1536, us in tiles of 128 and 256:
+    // 128 rows 176, 187, 256 rows 213, 235, 384 rows 275, 280, 512 rows 325,
+    // 322; gathered, where each tile looks its rows up: 192 rows 222, 223, 256
+    // rows 246, 244, 512 rows 356, 338)
     const bool big = M / E >= 192 && (N + 127) / 128 % 2 == 0;
     const int64_t slots = big ? 256 : 512;
     int64_t per = tile(big ? 256 : 128, 256);
@@ -881,6 +884,7 @@ WgradPlan wgrad_plan(int M, int N, int K, int E) {
         const int64_t rows = std::max<int64_t>((stages + want - 1) / want, 8) * kBK;
         if (rows < M) p.slice = (int)rows;
     }
+    if (p.slice >= M && big && !gathered && M / E < 448) per = tile(128, 256);    // (no slices: no workspace either way)
     p.parts = p.slice < M ? 2 * (M / p.slice) + 2 : 0;
     p.part_bytes = (int64_t)p.parts * N * K * 4;
     p.tiles = (p.slice < M ? M / p.slice + (int64_t)E : E) * per;
@@ -944,11 +948,11 @@ moe_status launch_grouped_dgrad(const GroupedArgs& g, void* ws, hipStream_t s) {
 }
 
 size_t grouped_wgrad_workspace_bytes(int M, int N, int K, int E) {
-    return (size_t)wgrad_plan(M, N, K, E).part_bytes;
+    return (size_t)wgrad_plan(M, N, K, E, false).part_bytes;    // the same where rows are gathered
 }
 
 moe_status launch_grouped_wgrad(const GroupedArgs& g, float* dw, bool accumulate, void* ws, hipStream_t s) {
-    const WgradPlan p = wgrad_plan(g.M, g.N, g.K, g.E);
+    const WgradPlan p = wgrad_plan(g.M, g.N, g.K, g.E, g.slots != nullptr);
     WgradParams P{};
     P.dy = g.dy;
     P.x = g.x;

@@ -183,6 +183,26 @@ def test_wgrad_gathered(counts, K, N, k):
     assert_within(got, ref, n * U32 * mag, "wgrad gathered")
 
 
+@pytest.mark.parametrize("counts", [[500, 0, 1301, 700], [300, 1, 0, 640]], ids=["long", "mean 235"])
+@pytest.mark.parametrize("gather", [False, True])
+def test_wgrad_wide(counts, gather):
+    """More tiles than CUs, none of them full at the edges: no slices."""
+    K, N, k = 4104, 1000, 3
+    g, off, M, live = problem(counts, K, N, seed=9)
+    assert B.moe_grouped_linear_wgrad_workspace_size(M, N, K, len(counts)) == 0
+    dy = randn(g, M, N)
+    if gather:
+        x = randn(g, M // k + 1, K)
+        slots = torch.randint(0, x.shape[0] * k, (M,), generator=g, device=DEV, dtype=torch.int32)
+        slots[2] = -1
+        rows, got = source_rows(x, slots, k, M), B.moe_grouped_linear_wgrad(dy, x, off, slots, k)
+    else:
+        x = randn(g, M, K)
+        rows, got = x.to(F64), B.moe_grouped_linear_wgrad(dy, x, off)
+    ref, mag, n = wgrad_ref(dy, rows, off, N, K)
+    assert_within(got, ref, n * U32 * mag, "wgrad wide")
+
+
 def test_offsets_outside_are_clamped():
     """Offsets below 0 or past M count as 0 or M; descending ones hold no rows."""
     g = gen_of(1)
