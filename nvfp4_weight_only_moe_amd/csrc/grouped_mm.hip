@@ -37,6 +37,7 @@
 #include "internal.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace moe {
 namespace {
@@ -591,6 +592,7 @@ struct WgradParams {
     int N, K, ntn, ntk;
     int slice;                    // rows of a slice of the reduction
     int accumulate;
+    int shared_lines;             // 64-byte lines of dW that two tiles share: through the L2
     float* dw;                    // [E][N][K]
     float* part;                  // fp32 [N][K] per slice of the experts that have two or more
     int parts;                    // how many fit (offsets that are not ascending could ask for more)
@@ -724,22 +726,39 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2) k_wgrad(WgradParams P) {
     // no better with 1 KB).
     static_assert(NI == 4 && W * 16 * kTurnRow <= kBRing + NSB * kBBytes, "the stages' memory");
     uint8_t* turn = smem + wave * 16 * kTurnRow;
+    const auto store = [&](auto shared_lines) {
 #pragma unroll
-    for (int mi = 0; mi < MI; ++mi) {
+        for (int mi = 0; mi < MI; ++mi) {
 #pragma unroll
-        for (int ni = 0; ni < NI; ++ni)
-            *reinterpret_cast<floatx4*>(turn + lrow * kTurnRow + ni * 64 + q * 16) = acc[mi][ni];
-        const int c = k0 + wn * 64 + lrow * 4;
+            for (int ni = 0; ni < NI; ++ni)
+                *reinterpret_cast<floatx4*>(turn + lrow * kTurnRow + ni * 64 + q * 16) = acc[mi][ni];
+            const int c = k0 + wn * 64 + lrow * 4;
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            const int n = n0 + (wm * MI + mi) * 16 + h * 4 + q;
-            floatx4 w = *reinterpret_cast<const floatx4*>(turn + (h * 4 + q) * kTurnRow + lrow * 16);
-            if (n >= P.N || c >= P.K) continue;
-            floatx4* p = reinterpret_cast<floatx4*>(base + (int64_t)n * P.K + c);
-            if (add) w += *p;
-            __builtin_nontemporal_store(w, p);
+            for (int h = 0; h < 4; ++h) {
+                const int n = n0 + (wm * MI + mi) * 16 + h * 4 + q;
+                floatx4 w = *reinterpret_cast<const floatx4*>(turn + (h * 4 + q) * kTurnRow + lrow * 16);
+                if (n >= P.N || c >= P.K) continue;
+                floatx4* p = reinterpret_cast<floatx4*>(base + (int64_t)n * P.K + c);
+                if (add) w += *p;
+                if constexpr (decltype(shared_lines)::value) {
+                    // floats by which the wave's columns begin inside a line of 64 bytes
+                    const int skew = ((int)(reinterpret_cast<uintptr_t>(p) >> 2) - lrow * 4) & 15;
+                    const bool shared = lrow * 4 < (-skew & 15) || lrow * 4 >= 64 - skew;
+                    // these first: after the others of their rows they cost half as
+                    // much again (179 us against 141); the comments between them
+                    // keep the compiler from making one store of the two
+                    if (shared) *p = w;
+                    asm volatile("; whole lines" ::: "memory");
+                    if (!shared) __builtin_nontemporal_store(w, p);
+                    asm volatile("; next rows" ::: "memory");
+                } else {
+                    __builtin_nontemporal_store(w, p);
+                }
+            }
         }
-    }
+    };
+    if (P.shared_lines) store(std::true_type{});
+    else store(std::false_type{});
 }
 
 // dW of the experts whose rows were cut into slices: the slices' sums, in order.
@@ -965,6 +984,13 @@ moe_status launch_grouped_wgrad(const GroupedArgs& g, float* dw, bool accumulate
     P.ntk = p.ntk;
     P.slice = p.slice;
     P.accumulate = accumulate;
+    // Rows of dW that begin inside a 64-byte line: the lines between two waves'
+    // columns leave by plain stores, to be whole when the L2 writes them; past
+    // the caches each half costs a read as well (64 experts, 656 x 4824, 32 rows:
+    // 241 us against 143; 54 experts, 1896 x 504: 68 against 43, 256 rows 73
+    // against 67).  With much to write and to read they leave the L2 before that
+    // (656 x 4824, 128 rows: 243 us against 231, 256 rows 311 against 243).
+    P.shared_lines = g.K % 16 != 0 && (g.M / g.E <= 64 || (int64_t)g.E * g.N * g.K * 4 <= 1 << 29);
     P.dw = dw;
     P.part = static_cast<float*>(ws);
     P.parts = p.parts;
